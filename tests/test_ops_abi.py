@@ -1,0 +1,245 @@
+"""The operator entry points (include/vit_ops.h) without a GPU: every declared function is exported, the
+Python structures have the C ones' layout, host validation refuses bad arguments before any CUDA
+call, and the frequency helper matches its formulas."""
+import ctypes
+import math
+import os
+import re
+import subprocess
+import tempfile
+
+import pytest
+import torch
+
+import vision_transformer_encoder_fwd_b200 as V
+from vision_transformer_encoder_fwd_b200 import ops
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+P = ctypes.c_void_p
+A = 1 << 16  # a 16-byte aligned address that no call may touch
+BF16, F16, F32, E4M3 = 0, 1, 2, 3
+
+
+def test_header_and_exports():
+    src = re.sub(r"/\*.*?\*/", "", open(os.path.join(ROOT, "include", "vit_ops.h")).read(), flags=re.S)
+    names = set(re.findall(r"\b(vit_op_\w+)\s*\(", src))
+    assert {"vit_op_rms_norm", "vit_op_rope", "vit_op_linear_fp8", "vit_op_attention_packed", "vit_op_poll"} <= names
+    V.load_library()
+    out = subprocess.run(["nm", "-D", "--defined-only", V.LIB_PATH], capture_output=True, text=True).stdout
+    assert names <= set(re.findall(r" T (vit_\w+)", out))
+    for n in names:
+        assert ops._fn(n[len("vit_op_"):])
+
+
+def test_struct_layouts_match_c():
+    fields = {"vit_rope_tensor": [f if f != "in_" else "in" for f, _ in V.VitRopeTensor._fields_],
+              "vit_attn_packed": [f for f, _ in V.VitAttnPacked._fields_]}
+    lines = "".join('printf("%%zu ", sizeof(%s));' % s + "".join('printf("%%zu ", offsetof(%s, %s));' % (s, f) for f in fs)
+                    for s, fs in fields.items())
+    with tempfile.TemporaryDirectory() as d:
+        c, exe = os.path.join(d, "p.c"), os.path.join(d, "p")
+        open(c, "w").write('#include <stdio.h>\n#include <stddef.h>\n#include "vit_ops.h"\nint main(void) {%s return 0;}' % lines)
+        subprocess.run(["gcc", "-std=c99", "-I", os.path.join(ROOT, "include"), c, "-o", exe], check=True)
+        got = [int(x) for x in subprocess.run([exe], capture_output=True, text=True, check=True).stdout.split()]
+    want = []
+    for s in (V.VitRopeTensor, V.VitAttnPacked):
+        want += [ctypes.sizeof(s)] + [getattr(s, f).offset for f, _ in s._fields_]
+    assert got == want
+
+
+def _norm(**kw):
+    a = dict(x=A, xt=BF16, xld=64, r=None, rld=0, h=None, hld=0, rt=0, w=A, wt=BF16, eps=1e-6, rows=4, D=64, out=A, ot=BF16,
+             old=64, sc=None)
+    a.update(kw)
+    return ops._fn("rms_norm")(a["x"], a["xt"], a["xld"], a["r"], a["rld"], a["h"], a["hld"], a["rt"], a["w"], a["wt"],
+                               a["eps"], a["rows"], a["D"], a["out"], a["ot"], a["old"], a["sc"], None)
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(xt=E4M3), V.VIT_E_UNSUPPORTED),
+    (dict(xt=7), V.VIT_E_UNSUPPORTED),
+    (dict(ot=F16), V.VIT_E_UNSUPPORTED),              # neither x's type nor e4m3
+    (dict(wt=F16), V.VIT_E_UNSUPPORTED),
+    (dict(r=A, h=A, rt=F16), V.VIT_E_UNSUPPORTED),
+    (dict(ot=E4M3), V.VIT_E_INVALID_ARG),              # 8-bit rows without scales
+    (dict(sc=A), V.VIT_E_INVALID_ARG),                 # scales without 8-bit rows
+    (dict(r=A), V.VIT_E_INVALID_ARG),
+    (dict(h=A), V.VIT_E_INVALID_ARG),
+    (dict(w=None), V.VIT_E_INVALID_ARG),
+    (dict(x=None), V.VIT_E_INVALID_ARG),
+    (dict(x=A + 1), V.VIT_E_INVALID_ARG),
+    (dict(r=A, h=A + 2, rt=F32, rld=64, hld=64), V.VIT_E_INVALID_ARG),
+    (dict(eps=-1.0), V.VIT_E_INVALID_ARG),
+    (dict(eps=math.nan), V.VIT_E_INVALID_ARG),
+    (dict(eps=math.inf), V.VIT_E_INVALID_ARG),
+    (dict(D=0), V.VIT_E_SHAPE),
+    (dict(D=32769, xld=32769, old=32769), V.VIT_E_SHAPE),
+    (dict(rows=-1), V.VIT_E_SHAPE),
+    (dict(xld=-64), V.VIT_E_SHAPE),
+    (dict(old=63), V.VIT_E_SHAPE),                     # output rows would overlap
+    (dict(r=A, h=A, rld=64, hld=8), V.VIT_E_SHAPE),
+    (dict(rows=0), V.VIT_OK),
+])
+def test_rms_norm_refusals(kw, expect):
+    assert _norm(**kw) == expect
+    assert V.load_library().vit_last_error() or expect == V.VIT_OK
+
+
+def test_quant_rows_refusals():
+    f = ops._fn("quant_rows")
+    assert f(A, E4M3, 64, 4, 64, A, 64, A, None) == V.VIT_E_UNSUPPORTED
+    assert f(A, BF16, 64, 4, 64, A, 64, None, None) == V.VIT_E_INVALID_ARG
+    assert f(A, BF16, 64, 4, 64, A, 64, A + 2, None) == V.VIT_E_INVALID_ARG
+    assert f(A, BF16, 64, 4, 64, A, 32, A, None) == V.VIT_E_SHAPE
+    assert f(A, BF16, 64, 0, 64, None, 64, None, None) == V.VIT_OK
+
+
+def _linear(**kw):
+    a = dict(A=A, lda=64, sa=A, W=A, ldw=64, sw=A, b=None, M=4, N=16, K=64, out=A, ldo=16, st=None)
+    a.update(kw)
+    return ops._fn("linear_fp8")(a["A"], a["lda"], a["sa"], a["W"], a["ldw"], a["sw"], a["b"], a["M"], a["N"], a["K"],
+                                 a["out"], a["ldo"], a["st"], 0, None)
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(K=8), V.VIT_E_SHAPE),
+    (dict(K=72, lda=80, ldw=80), V.VIT_E_SHAPE),
+    (dict(N=12), V.VIT_E_SHAPE),
+    (dict(M=-1), V.VIT_E_SHAPE),
+    (dict(lda=48), V.VIT_E_SHAPE),
+    (dict(lda=72), V.VIT_E_SHAPE),
+    (dict(ldw=72), V.VIT_E_SHAPE),
+    (dict(ldo=20), V.VIT_E_SHAPE),
+    (dict(ldo=8), V.VIT_E_SHAPE),
+    (dict(A=A + 8), V.VIT_E_INVALID_ARG),
+    (dict(W=A + 8), V.VIT_E_INVALID_ARG),
+    (dict(out=A + 8), V.VIT_E_INVALID_ARG),
+    (dict(b=A + 4), V.VIT_E_INVALID_ARG),
+    (dict(sa=None), V.VIT_E_INVALID_ARG),
+    (dict(sw=A + 4), V.VIT_E_INVALID_ARG),
+    (dict(st=A + 2), V.VIT_E_INVALID_ARG),
+    (dict(M=0), V.VIT_OK),
+    (dict(N=0), V.VIT_OK),
+])
+def test_linear_refusals(kw, expect):
+    assert _linear(**kw) == expect
+
+
+def _rope(T=4, d=64, rd=64, axes=1, layout=0, gain=1.0, type=BF16, pos=A, freqs=None, q=None, qin=A, qout=A, heads=2):
+    f = freqs if freqs is not None else (ctypes.c_double * 256)(*([0.5] * 256))
+    t = V.VitRopeTensor(qin, qout, heads * d, d, heads * d, d, heads)
+    return ops._fn("rope")(ctypes.byref(t), None, type, T, d, rd, pos, 0, axes, f if freqs is not False else None, layout,
+                           gain, 0, None)
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(type=E4M3), V.VIT_E_UNSUPPORTED),
+    (dict(layout=2), V.VIT_E_UNSUPPORTED),
+    (dict(rd=63), V.VIT_E_SHAPE),
+    (dict(rd=0), V.VIT_E_SHAPE),
+    (dict(rd=66), V.VIT_E_SHAPE),                      # more than the head
+    (dict(d=512, rd=258), V.VIT_E_SHAPE),
+    (dict(axes=3), V.VIT_E_SHAPE),                     # 32 pairs on three axes
+    (dict(axes=5), V.VIT_E_SHAPE),
+    (dict(axes=0), V.VIT_E_SHAPE),
+    (dict(T=-1), V.VIT_E_SHAPE),
+    (dict(heads=-1), V.VIT_E_SHAPE),
+    (dict(gain=math.nan), V.VIT_E_INVALID_ARG),
+    (dict(freqs=False), V.VIT_E_INVALID_ARG),
+    (dict(freqs=(ctypes.c_double * 32)(*([math.inf] * 32))), V.VIT_E_INVALID_ARG),
+    (dict(pos=None), V.VIT_E_INVALID_ARG),
+    (dict(pos=A + 2), V.VIT_E_INVALID_ARG),
+    (dict(qout=None), V.VIT_E_INVALID_ARG),
+    (dict(qin=A + 1), V.VIT_E_INVALID_ARG),
+    (dict(T=0), V.VIT_OK),
+    (dict(heads=0), V.VIT_OK),
+])
+def test_rope_refusals(kw, expect):
+    assert _rope(**kw) == expect
+
+
+def attn_args(**kw):
+    a = dict(q=A, k=A, v=A, out=A, q_token=128, q_head=64, k_token=128, k_head=64, v_token=128, v_head=64, out_token=128,
+             out_head=64, cu_q=A, cu_k=A, len_k=None, Tq=8, Tk=8, n=1, heads_q=2, heads_k=2, head_dim=64, type=BF16,
+             causal=0, max_q=0, scale=0.125, status=None, wait_ns=0)
+    a.update(kw)
+    return V.VitAttnPacked(**a)
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(type=F32), V.VIT_E_UNSUPPORTED),
+    (dict(head_dim=96), V.VIT_E_UNSUPPORTED),
+    (dict(heads_q=3), V.VIT_E_SHAPE),
+    (dict(heads_k=0), V.VIT_E_SHAPE),
+    (dict(heads_q=65536), V.VIT_E_SHAPE),
+    (dict(n=-1), V.VIT_E_SHAPE),
+    (dict(Tq=-1), V.VIT_E_SHAPE),
+    (dict(Tq=1 << 30), V.VIT_E_SHAPE),
+    (dict(Tk=1 << 30), V.VIT_E_SHAPE),
+    (dict(k_token=132), V.VIT_E_SHAPE),
+    (dict(v_head=-64), V.VIT_E_SHAPE),
+    (dict(out_token=1 << 38), V.VIT_E_SHAPE),
+    (dict(scale=0.0), V.VIT_E_INVALID_ARG),
+    (dict(scale=math.inf), V.VIT_E_INVALID_ARG),
+    (dict(scale=math.nan), V.VIT_E_INVALID_ARG),
+    (dict(q=None), V.VIT_E_INVALID_ARG),
+    (dict(k=None), V.VIT_E_INVALID_ARG),
+    (dict(cu_k=None), V.VIT_E_INVALID_ARG),
+    (dict(q=A + 8), V.VIT_E_INVALID_ARG),
+    (dict(out=A + 8), V.VIT_E_INVALID_ARG),
+    (dict(cu_q=A + 2), V.VIT_E_INVALID_ARG),
+    (dict(n=0), V.VIT_OK),
+    (dict(Tq=0), V.VIT_OK),
+])
+def test_attention_refusals(kw, expect):
+    assert ops._fn("attention_packed")(ctypes.byref(attn_args(**kw)), None) == expect
+
+
+def test_binding_refuses_cpu_tensors():
+    x = torch.zeros(2, 16, dtype=torch.bfloat16)
+    with pytest.raises(V.VitError) as e:
+        V.rms_norm(x, x[0])
+    assert e.value.status == V.VIT_E_INVALID_ARG
+    with pytest.raises(V.VitError):
+        V.quant_rows(x)
+
+
+def test_rope_frequencies():
+    """base^(-i/p), and its stretched forms, to the last few bits of a double."""
+    base, p, factor = 10000.0, 32, 8.0
+    plain = [base ** (-i / p) for i in range(p)]
+
+    def close(f, want):
+        assert f.dtype == torch.float64 and f.shape == (len(want),)
+        assert all(abs(a - b) <= 1e-14 * b for a, b in zip(f.tolist(), want))
+    close(V.rope_freqs(base, 2 * p), plain)
+    close(V.rope_freqs(base, 2 * p, scaling="linear", factor=factor), [f / factor for f in plain])
+    b2 = base * factor ** (p / (p - 1))
+    close(V.rope_freqs(base, 2 * p, scaling="base", factor=factor), [b2 ** (-i / p) for i in range(p)])
+    parts = []
+    for f in plain:
+        keep = min(1.0, max(0.0, (f * 4096 / (2 * math.pi) - 1.0) / 31.0))
+        parts.append(f / factor * (1 - keep) + f * keep)
+    close(V.rope_freqs(base, 2 * p, scaling="parts", factor=factor, original_len=4096), parts)
+    half = [base ** (-i / (p // 2)) for i in range(p // 2)]
+    close(V.rope_freqs(base, 2 * p, axes=2), half + half)
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(base=0.0), V.VIT_E_INVALID_ARG),
+    (dict(base=math.nan), V.VIT_E_INVALID_ARG),
+    (dict(rotary_dim=258), V.VIT_E_SHAPE),
+    (dict(rotary_dim=7), V.VIT_E_SHAPE),
+    (dict(axes=3), V.VIT_E_SHAPE),
+    (dict(scaling="linear", factor=0.0), V.VIT_E_INVALID_ARG),
+    (dict(scaling="parts", factor=2.0), V.VIT_E_INVALID_ARG),                     # no original length
+    (dict(scaling="parts", factor=2.0, original_len=64, beta_fast=1.0, beta_slow=1.0), V.VIT_E_INVALID_ARG),
+    (dict(scaling="base", factor=2.0, rotary_dim=2), V.VIT_E_SHAPE),
+    (dict(scaling="other"), V.VIT_E_UNSUPPORTED),
+])
+def test_rope_frequency_refusals(kw, expect):
+    a = dict(base=10000.0, rotary_dim=64)
+    a.update(kw)
+    with pytest.raises(V.VitError) as e:
+        V.rope_freqs(**a)
+    assert e.value.status == expect

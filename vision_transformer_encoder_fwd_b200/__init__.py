@@ -1,4 +1,4 @@
-"""Python binding of libvit_b200 (the C ABI in include/vit.h and include/vit_stages.h).
+"""Python binding of libvit_b200 (the C ABI in include/vit.h, vit_stages.h and vit_ops.h).
 
 Argument marshalling only: torch supplies device memory and streams; every step of the
 encoder runs in the library's CUDA kernels.  If the shared library is missing or cannot be
@@ -433,3 +433,7 @@ def stage_gelu(x, stream=None):
     _check("vit_stage_gelu", lib.vit_stage_gelu(_ptr(x), x.numel(), _ptr(y), _stream_handle(stream)))
     return y
 
+
+# ------------------------------------------------------------------ operators beside the encoder
+from .ops import (ROPE_LAYOUTS, ROPE_SCALINGS, VitAttnPacked, VitRopeTensor, attention_packed, linear_fp8,  # noqa: E402
+                  op_poll, quant_rows, rms_norm, rope, rope_freqs)

@@ -1,0 +1,408 @@
+// Host side of the operator entry points in include/vit_ops.h: checks, tensor maps, launches.
+#include <algorithm>
+#include <cmath>
+
+#include "../../include/vit_ops.h"
+#include "attention_packed.cuh"
+#include "host_common.cuh"
+#include "linear_fp8.cuh"
+#include "rope.cuh"
+#include "rows.cuh"
+
+using namespace vit;
+
+namespace {
+
+vit_status fail(vit_status st, const char* msg) {
+  set_err("%s", msg);
+  return st;
+}
+
+bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+size_t type_size(int t) { return t == VIT_DT_F32 ? 4 : (t == VIT_DT_E4M3 ? 1 : 2); }
+
+bool real_type(int t) { return t == VIT_DT_BF16 || t == VIT_DT_F16 || t == VIT_DT_F32; }
+
+int current_sms() {
+  int dev = 0;
+  cudaGetDevice(&dev);
+  return device_sms(dev);
+}
+
+// ------------------------------------------------------------------ rows
+// Layout of a row over threads: E values per access, NV accesses per thread, tpr threads a row.
+template <typename TX, int RMODE, bool OUT8>
+cudaError_t launch_rows(const RowsParams& p, bool vec, cudaStream_t s) {
+  auto go = [&](auto kernel, int tpr) {
+    const int block = tpr >= 128 ? tpr : 128;
+    const int64_t per = block / tpr;
+    return launch_pdl(kernel, dim3(static_cast<unsigned>((p.rows + per - 1) / per)), dim3(block), 0, s, p, tpr);
+  };
+  auto whole_warps = [](int threads) { return std::min(1024, std::max(32, (threads + 31) / 32 * 32)); };
+  // several rows share a block only at 32 threads a row
+  auto tpr_of = [&](int per_thread) {
+    const int t = whole_warps((p.D + per_thread - 1) / per_thread);
+    return t > 32 && t < 128 ? 128 : t;
+  };
+  if (vec) {
+    if (p.D <= 256) return go(rows_kernel<TX, RMODE, OUT8, 8, 1>, 32);
+    if (p.D <= 16384) return go(rows_kernel<TX, RMODE, OUT8, 8, 2>, tpr_of(16));
+    return go(rows_kernel<TX, RMODE, OUT8, 8, 4>, tpr_of(32));
+  }
+  if (p.D <= 8192) return go(rows_kernel<TX, RMODE, OUT8, 1, 8>, tpr_of(8));
+  return go(rows_kernel<TX, RMODE, OUT8, 1, 32>, tpr_of(32));
+}
+
+template <typename TX>
+cudaError_t launch_rows_t(const RowsParams& p, int rmode, bool vec, cudaStream_t s) {
+  const bool out8 = p.scales != nullptr;
+  if (rmode == 0) return out8 ? launch_rows<TX, 0, true>(p, vec, s) : launch_rows<TX, 0, false>(p, vec, s);
+  if (rmode == 1) return out8 ? launch_rows<TX, 1, true>(p, vec, s) : launch_rows<TX, 1, false>(p, vec, s);
+  return out8 ? launch_rows<TX, 2, true>(p, vec, s) : launch_rows<TX, 2, false>(p, vec, s);
+}
+
+vit_status run_rows(const RowsParams& p, int x_type, int r_type, int w_type, cudaStream_t s) {
+  const size_t xs = type_size(x_type);
+  const size_t os = p.scales != nullptr ? 1 : xs;
+  if (p.D < 1 || p.D > 32768 || p.rows < 0) return fail(VIT_E_SHAPE, "need 1 <= D <= 32768 and rows >= 0");
+  if (p.rows == 0) return VIT_OK;
+  if (p.rows > 0x7fffffffLL) return fail(VIT_E_SHAPE, "more than 2^31 - 1 rows");
+  if (!p.x || !p.out) return fail(VIT_E_INVALID_ARG, "x or out is NULL");
+  if (!aligned_to(p.x, xs) || !aligned_to(p.out, os) || !aligned_to(p.scales, 4))
+    return fail(VIT_E_INVALID_ARG, "a pointer is not aligned to its element type");
+  if (p.x_ld < 0 || (p.rows > 1 && p.out_ld < p.D)) return fail(VIT_E_SHAPE, "leading dimension too small");
+  bool vec = p.D % 8 == 0 && aligned16(p.x) && p.x_ld % 8 == 0 && aligned_to(p.out, os == 1 ? 8 : 16) && p.out_ld % 8 == 0;
+  if (p.w != nullptr) {
+    if (!aligned_to(p.w, type_size(w_type))) return fail(VIT_E_INVALID_ARG, "weight is not aligned to its type");
+    vec = vec && aligned16(p.w);
+  }
+  if (p.r != nullptr) {
+    if (!p.h) return fail(VIT_E_INVALID_ARG, "residual without residual_out");
+    if (!aligned_to(p.r, type_size(r_type)) || !aligned_to(p.h, type_size(r_type)))
+      return fail(VIT_E_INVALID_ARG, "the residual is not aligned to its type");
+    if (p.r_ld < 0 || (p.rows > 1 && p.h_ld < p.D)) return fail(VIT_E_SHAPE, "residual's leading dimension too small");
+    vec = vec && aligned16(p.r) && aligned16(p.h) && p.r_ld % 8 == 0 && p.h_ld % 8 == 0;
+  } else if (p.h != nullptr) {
+    return fail(VIT_E_INVALID_ARG, "residual_out without residual");
+  }
+  const int rmode = p.r == nullptr ? 0 : (r_type == x_type ? 1 : 2);
+  cudaError_t e;
+  if (x_type == VIT_DT_BF16)
+    e = launch_rows_t<__nv_bfloat16>(p, rmode, vec, s);
+  else if (x_type == VIT_DT_F16)
+    e = launch_rows_t<__half>(p, rmode, vec, s);
+  else
+    e = p.scales ? (rmode ? launch_rows<float, 1, true>(p, vec, s) : launch_rows<float, 0, true>(p, vec, s))
+                 : (rmode ? launch_rows<float, 1, false>(p, vec, s) : launch_rows<float, 0, false>(p, vec, s));
+  CK(e);
+  return VIT_OK;
+}
+
+// ------------------------------------------------------------------ tensor maps
+// 2-D map of 8-bit rows [rows, K]: box 128 bytes x box_rows, 128-byte swizzle; past the end: zeros.
+bool tmap_rows8(CUtensorMap* tm, const void* base, int64_t K, int64_t rows, int64_t ld, uint32_t box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld)};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(LIN8_BK), box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// 2-D map of a bf16 output [rows, cols]: boxes of 64 columns x 32 rows.
+bool tmap_out16(CUtensorMap* tm, void* base, int64_t cols, int64_t rows, int64_t ld) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
+  cuuint32_t box[2] = {64, 32};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// 3-D map of heads [tokens, heads, d] of a 16-bit type: box 64 values x 1 head x box_tokens.  The
+// values only move, so the type of the map does not matter.
+bool tmap_heads(CUtensorMap* tm, const void* base, int d, int heads, int64_t tokens, int64_t head_ld, int64_t tok_ld,
+                uint32_t box_tokens) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(tokens)};
+  // the stride of a dimension of one is never used, but has to be a valid one
+  if (heads == 1) head_ld = d;
+  if (tokens == 1) tok_ld = d;
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_ld) * 2, static_cast<cuuint64_t>(tok_ld) * 2};
+  cuuint32_t box[3] = {64, 1, box_tokens};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+vit_status no_map() { return fail(VIT_E_CUDA, "cuTensorMapEncodeTiled refused a tensor map"); }
+
+// ------------------------------------------------------------------ linear
+template <int BN>
+cudaError_t launch_lin8(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o, const Lin8Params& p, int* st,
+                        cudaStream_t s, int nsm) {
+  static std::atomic<uint64_t> attr_done{0};
+  constexpr int smem = Lin8Cfg<BN>::SMEM_BYTES;
+  cudaError_t e = set_smem_attr_once(lin8_tile_kernel<BN>, smem, attr_done);
+  if (e != cudaSuccess) return e;
+  const long long tiles = static_cast<long long>((p.M + LIN8_BM - 1) / LIN8_BM) * ((p.N + BN - 1) / BN);
+  return launch_pdl(lin8_tile_kernel<BN>, dim3(static_cast<unsigned>(std::min<long long>(tiles, nsm))),
+                    dim3(LIN8_THREADS), smem, s, a, b, o, p, st);
+}
+
+// ------------------------------------------------------------------ attention
+template <typename T, int HD>
+cudaError_t launch_attn_packed(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                               const AttnPackedParams& p, int* st, cudaStream_t s) {
+  static std::atomic<uint64_t> attr_done{0};
+  constexpr int smem = AttnPackedCfg<HD>::SMEM_BYTES;
+  cudaError_t e = set_smem_attr_once(attn_packed_kernel<T, HD>, smem, attr_done);
+  if (e != cudaSuccess) return e;
+  // n sequences of Tq rows in all need at most this many tiles
+  const long long tiles = static_cast<long long>(p.Tq) / ATT_BM + p.n;
+  return launch_pdl(attn_packed_kernel<T, HD>, dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(p.Hq)),
+                    dim3(ATT_THREADS), smem, s, q, k, v, p, st);
+}
+
+}  // namespace
+
+extern "C" {
+
+vit_status vit_op_rms_norm(const void* x, vit_dtype x_type, int64_t x_ld, const void* residual, int64_t residual_ld,
+                           void* residual_out, int64_t residual_out_ld, vit_dtype residual_type, const void* weight,
+                           vit_dtype weight_type, float eps, int64_t rows, int32_t D, void* out, vit_dtype out_type,
+                           int64_t out_ld, float* scales, vit_stream_t stream) {
+  if (!real_type(x_type)) return fail(VIT_E_UNSUPPORTED, "x must be bf16, fp16 or fp32");
+  if (out_type != x_type && out_type != VIT_DT_E4M3) return fail(VIT_E_UNSUPPORTED, "out must have x's type or e4m3");
+  if ((out_type == VIT_DT_E4M3) != (scales != nullptr) && rows != 0)
+    return fail(VIT_E_INVALID_ARG, "scales go with e4m3 rows, and only with them");
+  if (weight_type != x_type && weight_type != VIT_DT_F32)
+    return fail(VIT_E_UNSUPPORTED, "weight must have x's type or fp32");
+  if (residual != nullptr && residual_type != x_type && residual_type != VIT_DT_F32)
+    return fail(VIT_E_UNSUPPORTED, "the residual must have x's type or fp32");
+  if (!weight) return fail(VIT_E_INVALID_ARG, "weight is NULL");
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(VIT_E_INVALID_ARG, "eps must be finite and >= 0");
+  RowsParams p{x, residual, residual_out, weight, out, scales, x_ld, residual_ld, residual_out_ld, out_ld, rows, D, eps,
+               weight_type == VIT_DT_F32 ? 1 : 0};
+  return run_rows(p, x_type, residual_type, weight_type, reinterpret_cast<cudaStream_t>(stream));
+}
+
+vit_status vit_op_quant_rows(const void* x, vit_dtype x_type, int64_t x_ld, int64_t rows, int32_t D, void* out,
+                             int64_t out_ld, float* scales, vit_stream_t stream) {
+  if (!real_type(x_type)) return fail(VIT_E_UNSUPPORTED, "x must be bf16, fp16 or fp32");
+  if (!scales && rows != 0) return fail(VIT_E_INVALID_ARG, "scales is NULL");
+  RowsParams p{x, nullptr, nullptr, nullptr, out, scales, x_ld, 0, 0, out_ld, rows, D, 0.f, 0};
+  return run_rows(p, x_type, x_type, x_type, reinterpret_cast<cudaStream_t>(stream));
+}
+
+vit_status vit_op_linear_fp8(const void* A, int64_t lda, const float* a_scales, const void* W, int64_t ldw,
+                             const float* w_scales, const float* bias, int32_t M, int32_t N, int32_t K, void* out,
+                             int64_t ldo, int32_t* status, uint64_t wait_ns, vit_stream_t stream) {
+  if (M < 0 || N < 0 || K < 16 || K % 16 || N % 8)
+    return fail(VIT_E_SHAPE, "need M, N >= 0, N a multiple of 8, K >= 16 and a multiple of 16");
+  if (M == 0 || N == 0) return VIT_OK;
+  if (!A || !a_scales || !W || !w_scales || !out) return fail(VIT_E_INVALID_ARG, "NULL pointer");
+  if (!aligned16(A) || !aligned16(W) || !aligned16(out) || !aligned16(w_scales) || !aligned16(bias) ||
+      !aligned_to(a_scales, 4) || !aligned_to(status, 4))
+    return fail(VIT_E_INVALID_ARG, "A, W, out, w_scales and bias must be 16-byte aligned");
+  if ((M > 1 && lda < K) || (N > 1 && ldw < K) || (M > 1 && ldo < N) || lda % 16 || ldw % 16 || ldo % 8)
+    return fail(VIT_E_SHAPE, "leading dimensions: at least a row, lda and ldw multiples of 16, ldo of 8");
+  const int nsm = current_sms();
+  Lin8Params p{M, N, K, a_scales, w_scales, bias, wait_ns};
+  CUtensorMap ta, tb, to;
+  if (!tmap_rows8(&ta, A, K, M, std::max<int64_t>(lda, K), LIN8_BM) ||
+      !tmap_rows8(&tb, W, K, N, std::max<int64_t>(ldw, K), 128) || !tmap_out16(&to, out, N, M, std::max<int64_t>(ldo, N)))
+    return no_map();
+  CK(launch_lin8<128>(ta, tb, to, p, status, reinterpret_cast<cudaStream_t>(stream), nsm));
+  return VIT_OK;
+}
+
+vit_status vit_op_rope_freqs(double base, int32_t pairs, int32_t axes, int32_t scaling, double factor,
+                             double original_len, double beta_fast, double beta_slow, double* freqs) {
+  if (!freqs || !(base > 0.0) || !std::isfinite(base)) return fail(VIT_E_INVALID_ARG, "need base > 0 and room for freqs");
+  if (pairs < 1 || axes < 1 || axes > 4 || pairs % axes || pairs > ROPE_MAX_PAIRS)
+    return fail(VIT_E_SHAPE, "need 1..128 pairs, a multiple of 1..4 axes");
+  if (scaling < VIT_ROPE_PLAIN || scaling > VIT_ROPE_PARTS) return fail(VIT_E_UNSUPPORTED, "unknown scaling");
+  if (scaling != VIT_ROPE_PLAIN && !(factor > 0.0 && std::isfinite(factor)))
+    return fail(VIT_E_INVALID_ARG, "factor must be positive");
+  if (scaling == VIT_ROPE_PARTS && !(original_len > 0.0 && beta_fast > beta_slow))
+    return fail(VIT_E_INVALID_ARG, "need original_len > 0 and beta_fast > beta_slow");
+  const int p = pairs / axes;
+  if (scaling == VIT_ROPE_BASE) {
+    if (p < 2) return fail(VIT_E_SHAPE, "a larger base needs two pairs an axis");
+    base *= std::pow(factor, static_cast<double>(p) / (p - 1));
+  }
+  for (int i = 0; i < p; ++i) {
+    double f = std::pow(base, -static_cast<double>(i) / p);
+    if (scaling == VIT_ROPE_LINEAR) f /= factor;
+    if (scaling == VIT_ROPE_PARTS) {
+      const double turns = f * original_len / 6.283185307179586476925;
+      const double keep = std::min(1.0, std::max(0.0, (turns - beta_slow) / (beta_fast - beta_slow)));
+      f = f / factor * (1.0 - keep) + f * keep;
+    }
+    for (int a = 0; a < axes; ++a) freqs[a * p + i] = f;
+  }
+  return VIT_OK;
+}
+
+vit_status vit_op_rope(const vit_rope_tensor* q, const vit_rope_tensor* k, vit_dtype type, int64_t T, int32_t head_dim,
+                       int32_t rotary_dim, const void* positions, int32_t pos64, int32_t axes, const double* freqs,
+                       int32_t layout, float gain, int32_t inverse, vit_stream_t stream) {
+  if (!real_type(type)) return fail(VIT_E_UNSUPPORTED, "heads must be bf16, fp16 or fp32");
+  if (layout != VIT_ROPE_HALF && layout != VIT_ROPE_INTERLEAVED) return fail(VIT_E_UNSUPPORTED, "unknown layout");
+  if (T < 0 || axes < 1 || axes > 4 || rotary_dim < 2 || rotary_dim % 2 || rotary_dim > 2 * ROPE_MAX_PAIRS ||
+      head_dim < rotary_dim || head_dim > 4096 || (rotary_dim / 2) % axes)
+    return fail(VIT_E_SHAPE, "rotary_dim: even, 2..256, at most head_dim (at most 4096), pairs a multiple of 1..4 axes");
+  if (!freqs) return fail(VIT_E_INVALID_ARG, "freqs is NULL");
+  if (!std::isfinite(gain)) return fail(VIT_E_INVALID_ARG, "gain must be finite");
+  const vit_rope_tensor* tq[2] = {q, k};
+  const int n = rotary_dim / 2;
+  const int e = type == VIT_DT_F32 ? 4 : 8;
+  bool vec = (layout == VIT_ROPE_HALF ? n : rotary_dim) % e == 0 && (head_dim - rotary_dim) % e == 0;
+  RopeParams p{};
+  for (int i = 0; i < 2; ++i) {
+    if (!tq[i] || !tq[i]->in || tq[i]->heads == 0) continue;
+    const vit_rope_tensor& t = *tq[i];
+    if (t.heads < 0) return fail(VIT_E_SHAPE, "negative number of heads");
+    if (!t.out || !aligned_to(t.in, type_size(type)) || !aligned_to(t.out, type_size(type)))
+      return fail(VIT_E_INVALID_ARG, "output NULL, or a pointer not aligned to its type");
+    p.in[i] = t.in;
+    p.out[i] = t.out;
+    p.in_tok[i] = t.in_token;
+    p.in_head[i] = t.in_head;
+    p.out_tok[i] = t.out_token;
+    p.out_head[i] = t.out_head;
+    p.heads[i] = t.heads;
+    vec = vec && aligned16(t.in) && aligned16(t.out) && t.in_token % e == 0 && t.in_head % e == 0 &&
+          t.out_token % e == 0 && t.out_head % e == 0;
+  }
+  if (T == 0 || p.heads[0] + p.heads[1] == 0) return VIT_OK;
+  if (!positions || !aligned_to(positions, pos64 ? 8 : 4)) return fail(VIT_E_INVALID_ARG, "positions NULL or misaligned");
+  for (int i = 0; i < n; ++i) {
+    if (!std::isfinite(freqs[i])) return fail(VIT_E_INVALID_ARG, "a frequency is not finite");
+    // 2^64 times the fraction of a turn, in the 64-bit mantissa of long double
+    long double t = static_cast<long double>(freqs[i]) * 0.15915494309189533576888376337251436L;
+    if (!(t >= 0.0L && t < 1.0L)) t -= floorl(t);
+    t = t * 18446744073709551616.0L + 0.5L;
+    p.turn[i] = t >= 18446744073709551616.0L ? 0ull : static_cast<unsigned long long>(t);
+  }
+  p.pos = positions;
+  p.T = T;
+  p.d = head_dim;
+  p.rd = rotary_dim;
+  p.axes = axes;
+  p.pos64 = pos64 != 0;
+  p.sign = inverse ? -1.f : 1.f;
+  p.gain = gain;
+  // tokens a block: enough pairs for one sine and cosine per thread, but at least four blocks an SM
+  // while the tokens last
+  const int64_t spread = std::max<int64_t>(1, T / (4 * current_sms()));
+  p.tokens = static_cast<int>(std::min<int64_t>(spread, std::max(1, ROPE_THREADS / n)));
+  const int64_t blocks = (T + p.tokens - 1) / p.tokens;
+  if (blocks > 0x7fffffffLL) return fail(VIT_E_SHAPE, "too many tokens");
+  const size_t smem = static_cast<size_t>(p.tokens) * n * sizeof(float2);
+  auto go = [&](auto kernel) {
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(ROPE_THREADS), smem,
+                      reinterpret_cast<cudaStream_t>(stream), p);
+  };
+  cudaError_t err;
+  const bool half = layout == VIT_ROPE_HALF;
+  if (type == VIT_DT_BF16)
+    err = half ? (vec ? go(rope_kernel<__nv_bfloat16, true, 8>) : go(rope_kernel<__nv_bfloat16, true, 1>))
+               : (vec ? go(rope_kernel<__nv_bfloat16, false, 8>) : go(rope_kernel<__nv_bfloat16, false, 1>));
+  else if (type == VIT_DT_F16)
+    err = half ? (vec ? go(rope_kernel<__half, true, 8>) : go(rope_kernel<__half, true, 1>))
+               : (vec ? go(rope_kernel<__half, false, 8>) : go(rope_kernel<__half, false, 1>));
+  else
+    err = half ? (vec ? go(rope_kernel<float, true, 4>) : go(rope_kernel<float, true, 1>))
+               : (vec ? go(rope_kernel<float, false, 4>) : go(rope_kernel<float, false, 1>));
+  CK(err);
+  return VIT_OK;
+}
+
+vit_status vit_op_attention_packed(const vit_attn_packed* a, vit_stream_t stream) {
+  if (!a) return fail(VIT_E_INVALID_ARG, "arguments are NULL");
+  if (a->type != VIT_DT_BF16 && a->type != VIT_DT_F16) return fail(VIT_E_UNSUPPORTED, "heads must be bf16 or fp16");
+  if (a->head_dim != 64 && a->head_dim != 128) return fail(VIT_E_UNSUPPORTED, "head_dim must be 64 or 128");
+  if (a->n < 0 || a->Tq < 0 || a->Tk < 0 || a->Tq > 0x3fffffffLL || a->Tk > 0x3fffffffLL || a->heads_q < 1 ||
+      a->heads_k < 1 || a->heads_q % a->heads_k || a->heads_q > 65535)
+    return fail(VIT_E_SHAPE, "need n >= 0, 0 <= Tq, Tk < 2^30, heads_q (at most 65535) a multiple of heads_k >= 1");
+  if (!(a->scale > 0.f) || !std::isfinite(a->scale)) return fail(VIT_E_INVALID_ARG, "scale must be positive and finite");
+  if (a->n == 0 || a->Tq == 0) return VIT_OK;
+  if (!a->q || !a->out || !a->cu_q || !a->cu_k || (a->Tk > 0 && (!a->k || !a->v)))
+    return fail(VIT_E_INVALID_ARG, "NULL pointer");
+  if (!aligned16(a->q) || !aligned16(a->k) || !aligned16(a->v) || !aligned16(a->out) || !aligned_to(a->cu_q, 4) ||
+      !aligned_to(a->cu_k, 4) || !aligned_to(a->len_k, 4) || !aligned_to(a->status, 4))
+    return fail(VIT_E_INVALID_ARG, "q, k, v and out must be 16-byte aligned");
+  const int64_t strides[8] = {a->q_token, a->q_head, a->k_token, a->k_head, a->v_token, a->v_head, a->out_token, a->out_head};
+  for (int64_t s : strides)
+    if (s % 8 || s < 0 || s >= (1LL << 38)) return fail(VIT_E_SHAPE, "strides must be multiples of 8, not negative");
+  if (static_cast<int64_t>(a->n) + a->Tq / ATT_BM > 0x7fffffffLL) return fail(VIT_E_SHAPE, "too many sequences");
+  AttnPackedParams p{};
+  p.q = a->q;
+  p.k = a->k;
+  p.v = a->v;
+  p.out = a->out;
+  p.q_tok = a->q_token;
+  p.q_head = a->q_head;
+  p.k_tok = a->k_token;
+  p.k_head = a->k_head;
+  p.v_tok = a->v_token;
+  p.v_head = a->v_head;
+  p.o_tok = a->out_token;
+  p.o_head = a->out_head;
+  p.cu_q = a->cu_q;
+  p.cu_k = a->cu_k;
+  p.len_k = a->len_k;
+  p.n = a->n;
+  p.Tq = static_cast<int>(a->Tq);
+  p.Tk = static_cast<int>(a->Tk);
+  p.Hq = a->heads_q;
+  p.Hkv = a->heads_k;
+  p.causal = a->causal != 0;
+  p.scale_log2 = a->scale * 1.4426950408889634f;
+  p.wait_ns = a->wait_ns;
+  CUtensorMap tq, tk, tv;
+  // without keys nothing is loaded: any valid map will do
+  const void* kb = a->Tk > 0 ? a->k : a->q;
+  const void* vb = a->Tk > 0 ? a->v : a->q;
+  const int64_t tkeys = std::max<int64_t>(1, a->Tk);
+  if (!tmap_heads(&tq, a->q, a->head_dim, a->heads_q, a->Tq, a->q_head, a->q_token, ATT_BM) ||
+      !tmap_heads(&tk, kb, a->head_dim, a->heads_k, tkeys, a->k_head, a->k_token, 64) ||
+      !tmap_heads(&tv, vb, a->head_dim, a->heads_k, tkeys, a->v_head, a->v_token, 64))
+    return no_map();
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (a->type == VIT_DT_BF16)
+    e = a->head_dim == 64 ? launch_attn_packed<__nv_bfloat16, 64>(tq, tk, tv, p, a->status, s)
+                          : launch_attn_packed<__nv_bfloat16, 128>(tq, tk, tv, p, a->status, s);
+  else
+    e = a->head_dim == 64 ? launch_attn_packed<__half, 64>(tq, tk, tv, p, a->status, s)
+                          : launch_attn_packed<__half, 128>(tq, tk, tv, p, a->status, s);
+  CK(e);
+  return VIT_OK;
+}
+
+vit_status vit_op_poll(vit_stream_t stream) {
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int v = 0;
+  const int zero = 0;
+  CK(cudaMemcpyFromSymbolAsync(&v, g_op_status, sizeof(v), 0, cudaMemcpyDeviceToHost, s));
+  CK(cudaStreamSynchronize(s));
+  if (v == 0) return VIT_OK;
+  CK(cudaMemcpyToSymbolAsync(g_op_status, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s));
+  CK(cudaStreamSynchronize(s));
+  set_err("a kernel gave up on a pipeline wait (site 0x%x)", v);
+  return VIT_E_DEVICE_TIMEOUT;
+}
+
+}  // extern "C"

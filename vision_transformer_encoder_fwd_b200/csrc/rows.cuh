@@ -1,0 +1,208 @@
+// Root-mean-square norm of rows with the residual's addition, and rows quantised to 8 bits.
+//
+//   h = x + r                        (r optional; h is stored back in r's type)
+//   y = h * w / sqrt(mean(h^2) + eps)
+//   out = y                          (rounded to x's type), or
+//   s = max(max_j |y_j|, 2^-100) / 448,  out_j = e4m3(y_j / s)   (448: the largest e4m3 value)
+// and the same without the norm (y = x) for quantising weights and activations.
+//
+// The sum of squares, the norm and the largest magnitude are taken from h in fp32, before its
+// rounding.  Both reductions run in one exchange: the common factor 1/sqrt(...) is positive, so
+// max |y| = max |h w| / sqrt(...).
+//
+// Bound: bytes (x, r in; h, out written), so each row is read once into registers (8 values per
+// 16-byte load of a 16-bit type) and stays there.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include <type_traits>
+
+#include "common.cuh"
+
+namespace vit {
+
+constexpr float kE4m3Max = 448.0f;
+constexpr float kRowAmaxMin = 7.888609052210118e-31f;  // 2^-100: keeps 448 / amax finite
+
+template <typename T>
+__device__ __forceinline__ float to_f32(T v);
+template <>
+__device__ __forceinline__ float to_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <>
+__device__ __forceinline__ float to_f32<__half>(__half v) { return __half2float(v); }
+
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+
+// N consecutive values as fp32; VEC: 16-byte aligned, N * sizeof(T) a multiple of 16.
+template <typename T, int N, bool VEC>
+__device__ __forceinline__ void load_f32(const T* p, float (&v)[N]) {
+  if constexpr (VEC) {
+    constexpr int PER = 16 / sizeof(T);
+#pragma unroll
+    for (int i = 0; i < N / PER; ++i) {
+      const uint4 w = reinterpret_cast<const uint4*>(p)[i];
+      const T* e = reinterpret_cast<const T*>(&w);
+#pragma unroll
+      for (int j = 0; j < PER; ++j) v[i * PER + j] = to_f32<T>(e[j]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = to_f32<T>(p[i]);
+  }
+}
+
+template <typename T, int N, bool VEC>
+__device__ __forceinline__ void store_f32(T* p, const float (&v)[N]) {
+  if constexpr (VEC) {
+    constexpr int PER = 16 / sizeof(T);
+#pragma unroll
+    for (int i = 0; i < N / PER; ++i) {
+      uint4 w;
+      T* e = reinterpret_cast<T*>(&w);
+#pragma unroll
+      for (int j = 0; j < PER; ++j) e[j] = from_f32<T>(v[i * PER + j]);
+      reinterpret_cast<uint4*>(p)[i] = w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) p[i] = from_f32<T>(v[i]);
+  }
+}
+
+// Two values to e4m3 (nearest even, saturating; NaN stays NaN), the first in the low byte.
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+
+// The larger of two values, or NaN if one is: a row's largest magnitude keeps a NaN, as its scale does.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+struct RowsParams {
+  const void* x;
+  const void* r;   // residual in, or NULL
+  void* h;         // residual out (may be r)
+  const void* w;   // weight, or NULL: no norm
+  void* out;
+  float* scales;   // NULL: out has x's type
+  int64_t x_ld, r_ld, h_ld, out_ld;
+  int64_t rows;
+  int D;
+  float eps;
+  int w_f32;       // weight type: fp32, else x's type
+};
+
+// One row per group of `tpr` threads (a power of two, or the whole block); NV vectors of E values
+// per thread, vector v of thread t at element (v * tpr + t) * E.
+// RMODE: 0 no residual, 1 residual of x's type, 2 fp32 residual.
+template <typename TX, int RMODE, bool OUT8, int E, int NV>
+__global__ void __launch_bounds__(1024) rows_kernel(RowsParams p, int tpr) {
+  using TR = typename std::conditional<RMODE == 2, float, TX>::type;
+  constexpr bool VEC = E > 1;
+  __shared__ float2 part[32];
+  const int grp = threadIdx.x / tpr;
+  const int t = threadIdx.x - grp * tpr;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x / tpr) + grp;
+  pdl_wait();
+  pdl_launch_dependents();
+  const bool live = row < p.rows;
+  const bool norm = p.w != nullptr;
+  float h[NV][E], g[NV][E];
+  float ss = 0.f, top = 0.f;
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int c = (v * tpr + t) * E;
+    if (live && c < p.D) {
+      load_f32<TX, E, VEC>(static_cast<const TX*>(p.x) + row * p.x_ld + c, h[v]);
+      if (RMODE != 0) {
+        float r[E];
+        load_f32<TR, E, VEC>(static_cast<const TR*>(p.r) + row * p.r_ld + c, r);
+#pragma unroll
+        for (int i = 0; i < E; ++i) h[v][i] += r[i];
+      }
+      if (norm) {
+        if (p.w_f32)
+          load_f32<float, E, VEC>(static_cast<const float*>(p.w) + c, g[v]);
+        else
+          load_f32<TX, E, VEC>(static_cast<const TX*>(p.w) + c, g[v]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < E; ++i) h[v][i] = g[v][i] = 0.f;
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int c = (v * tpr + t) * E;
+    if (RMODE != 0 && live && c < p.D)
+      store_f32<TR, E, VEC>(static_cast<TR*>(p.h) + row * p.h_ld + c, h[v]);
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      ss = fmaf(h[v][i], h[v][i], ss);
+      if (norm) h[v][i] *= g[v][i];
+      if (OUT8) top = max_nan(top, fabsf(h[v][i]));
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    if (o < tpr) {
+      ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      if (OUT8) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+    }
+  }
+  if (tpr > 32) {
+    const int warp = threadIdx.x >> 5;
+    if ((threadIdx.x & 31) == 0) part[warp] = make_float2(ss, top);
+    __syncthreads();
+    const int w0 = grp * (tpr >> 5);
+    ss = 0.f;
+    top = 0.f;
+    for (int i = 0; i < (tpr >> 5); ++i) {
+      const float2 q = part[w0 + i];
+      ss += q.x;
+      top = max_nan(top, q.y);
+    }
+  }
+  if (!live) return;
+  const float rstd = norm ? rsqrtf(ss / static_cast<float>(p.D) + p.eps) : 1.0f;
+  float mul = 1.0f;  // on top of rstd: their product could overflow where the values do not
+  if (OUT8) {
+    const float amax = max_nan(top * rstd, kRowAmaxMin);
+    mul = kE4m3Max / amax;
+    if (t == 0) p.scales[row] = amax / kE4m3Max;
+  }
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int c = (v * tpr + t) * E;
+    if (c >= p.D) continue;
+#pragma unroll
+    for (int i = 0; i < E; ++i) h[v][i] = h[v][i] * rstd * mul;
+    if (OUT8) {
+      uint8_t* o = static_cast<uint8_t*>(p.out) + row * p.out_ld + c;
+      if constexpr (E == 8) {
+        *reinterpret_cast<uint2*>(o) = make_uint2(e4m3x2(h[v][0], h[v][1]) | e4m3x2(h[v][2], h[v][3]) << 16,
+                                                  e4m3x2(h[v][4], h[v][5]) | e4m3x2(h[v][6], h[v][7]) << 16);
+      } else {
+        for (int i = 0; i < E; ++i) o[i] = static_cast<uint8_t>(e4m3x2(h[v][i], 0.f));
+      }
+    } else {
+      store_f32<TX, E, VEC>(static_cast<TX*>(p.out) + row * p.out_ld + c, h[v]);
+    }
+  }
+}
+
+}  // namespace vit

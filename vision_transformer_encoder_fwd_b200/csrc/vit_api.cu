@@ -29,61 +29,13 @@
 #include "aux_kernels.cuh"
 #include "dense_head.cuh"
 #include "gemm.cuh"
+#include "host_common.cuh"
 
 using namespace vit;
 
 namespace {
 
-thread_local std::string g_err;
-
-void set_err(const char* fmt, ...) {
-  char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof(buf), fmt, ap);
-  va_end(ap);
-  g_err = buf;
-}
-
-#define CK(call)                                                                              \
-  do {                                                                                        \
-    cudaError_t e_ = (call);                                                                  \
-    if (e_ != cudaSuccess) {                                                                  \
-      set_err("%s failed: %s (%s:%d)", #call, cudaGetErrorString(e_), __FILE__, __LINE__);     \
-      return VIT_E_CUDA;                                                                      \
-    }                                                                                         \
-  } while (0)
-
-#define CKL()                                                                                 \
-  do {                                                                                        \
-    cudaError_t e_ = cudaGetLastError();                                                      \
-    if (e_ != cudaSuccess) {                                                                  \
-      set_err("kernel launch failed: %s (%s:%d)", cudaGetErrorString(e_), __FILE__, __LINE__); \
-      return VIT_E_CUDA;                                                                      \
-    }                                                                                         \
-  } while (0)
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
-
 // ------------------------------------------------------------------ TMA descriptor encoding
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  if (fn == nullptr) {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
-  }
-  return fn;
-}
-
 // 2-D bf16 map over a row-major [rows, cols] matrix with leading dimension ld (elements);
 // box = box_cols x box_rows with box_cols * 2 bytes == 128 (one 128-byte swizzle row).
 bool tmap_2d(CUtensorMap* tm, const void* base, uint64_t cols, uint64_t rows, uint64_t ld, uint32_t box_cols,
@@ -165,50 +117,6 @@ bool tmap_qkv3d(CUtensorMap* tm, const void* base, int B, int T, int D) {
 }
 
 // ------------------------------------------------------------------ launch helpers
-int device_sms(int dev) {
-  int n = 0;
-  cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-  return n > 0 ? n : 1;
-}
-
-template <typename K>
-cudaError_t set_smem_attr_once(K kernel, int bytes, std::atomic<uint64_t>& done) {
-  int dev = 0;
-  cudaGetDevice(&dev);
-  const uint64_t bit = 1ull << (dev & 63);
-  if (done.load() & bit) return cudaSuccess;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess) done.fetch_or(bit);
-  return e;
-}
-
-// Programmatic dependent launch for the tensor-core kernels, which call pdl_wait before they touch
-// global memory: each may be scheduled, and run its prologue (barrier set-up, tensor-memory
-// allocation), while the kernel before it in the stream finishes.  VIT_B200_PDL=0 in the
-// environment launches them in plain stream order instead.
-bool pdl_enabled() {
-  static const bool on = [] {
-    const char* e = std::getenv("VIT_B200_PDL");
-    return !(e != nullptr && e[0] == '0');
-  }();
-  return on;
-}
-
-template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, const Args&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = pdl_enabled() ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 template <int BN, int MODE, int XBUF = 2>
 cudaError_t launch_gemm_t(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o1, const CUtensorMap& o2,
                           int M, int N, int K, const EpiParams& ep, int* st, cudaStream_t s, int nsm) {
