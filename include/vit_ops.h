@@ -7,9 +7,9 @@
  *
  * Conventions as in vit.h: caller-owned device memory of the current device, work enqueued on
  * `stream` without synchronising, host validation before any launch.  Nothing is allocated and
- * nothing is kept from one call for the next, so calls may run side by side on any streams and be
- * captured into CUDA graphs.  Where a call has no work (no rows, no tokens) it returns VIT_OK
- * and enqueues nothing.
+ * nothing is kept from one call for the next, so calls may run side by side on any streams (with
+ * a workspace each where one is taken) and be captured into CUDA graphs.  Where a call has no work
+ * (no rows, no tokens) it returns VIT_OK and enqueues nothing.
  *   - Strides are in elements; the last dimension is contiguous.
  *   - `status`: device int32, zero at the start, that a kernel sets when one of its pipeline waits
  *     gives up and that later kernels on the same word check on entry (they return without work
@@ -110,9 +110,12 @@ vit_status vit_op_rope(const vit_rope_tensor *q, const vit_rope_tensor *k, vit_d
  *   cu_q, cu_k: device int32 [n + 1], not decreasing; len_k: device int32 [n].  Read on the device
  *   (a captured call takes new lengths on replay); values outside the buffers are clamped.
  *   max_q: the longest query length if the caller knows it, 0 if not.  Only the choice of kernels
- *   goes by it: a wrong value costs time, not results.
+ *   goes by it (few query rows per sequence, as single tokens over a cache, run on a kernel that
+ *   splits the keys' axis over the GPU): a wrong value costs time, not results.
+ *   workspace: vit_op_attention_packed_workspace bytes of device memory, 16-byte aligned, that no
+ *   other call uses before this one has run; needs no preparation.
  * Scores, softmax statistics and sums are fp32; the softmax weights are rounded to `type` for
- * the product with V, the result once. */
+ * the product with V (with few query rows: to twice its precision), the result once. */
 typedef struct vit_attn_packed {
   const void *q, *k, *v;
   void *out;
@@ -123,7 +126,14 @@ typedef struct vit_attn_packed {
   float scale;
   int32_t *status;
   uint64_t wait_ns;
+  void *workspace;
+  size_t workspace_bytes;
 } vit_attn_packed;
+
+/* Workspace of a call with these arguments on the current device: 0 where none is used.  Depends on
+ * max_q, heads_q, heads_k and head_dim (at most 10 MB), not on numbers of tokens or lengths. */
+vit_status vit_op_attention_packed_workspace(const vit_attn_packed *a, size_t *bytes);
+
 vit_status vit_op_attention_packed(const vit_attn_packed *a, vit_stream_t stream);
 
 /* Synchronise `stream`, then read and clear the current device's library status word (the one that

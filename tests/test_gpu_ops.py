@@ -680,3 +680,23 @@ def test_prompt_and_token_steps_of_a_layer():
             # two kernels, the same inputs: each within its tolerance of the exact result (values up to 5)
             assert (whole - token).abs().max() <= 2 * (3 * 2.0 ** -8 + 3e-4) * 5
     V.op_poll()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_attention_rows_wait_expiry_is_reported(d):
+    """The same for the kernel of few query rows, whose warps meet at the end of each item."""
+    V, g = lib(), gen(24)
+    n, lk = 40, 900
+    q = randn(g, n, 4, d, dtype=torch.bfloat16)
+    k, v = randn(g, n * lk, 2, d, dtype=torch.bfloat16), randn(g, n * lk, 2, d, dtype=torch.bfloat16)
+    cu_q, cu_k = cum([1] * n), cum([lk] * n)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    V.attention_packed(q, k, v, cu_q, cu_k, max_q=1, status=st, wait_ns=200)
+    torch.cuda.synchronize()
+    assert 0x500 < int(st.item()) < 0x600
+    out = torch.full_like(q, 0.5)
+    V.attention_packed(q, k, v, cu_q, cu_k, max_q=1, status=st, out=out)
+    assert (out == 0.5).all()
+    V.attention_packed(q, k, v, cu_q, cu_k, max_q=1, out=out)
+    V.op_poll()
+    check_attn(out, q, k, v, list(range(n)), cu_k.tolist(), [1] * n, [lk] * n, False, d ** -0.5)

@@ -4,6 +4,7 @@
 
 #include "../../include/vit_ops.h"
 #include "attention_packed.cuh"
+#include "attention_rows.cuh"
 #include "host_common.cuh"
 #include "linear_fp8.cuh"
 #include "rope.cuh"
@@ -173,6 +174,46 @@ cudaError_t launch_attn_packed(const CUtensorMap& q, const CUtensorMap& k, const
                     dim3(ATT_THREADS), smem, s, q, k, v, p, st);
 }
 
+// Few query rows per sequence (max_q queries of the heads that share a key head) go to the row kernel.
+constexpr int64_t kRowsKernelMax = 64;
+bool takes_rows_kernel(const vit_attn_packed* a) {
+  const int64_t group = a->heads_q / a->heads_k;
+  return a->max_q > 0 && a->max_q * group <= kRowsKernelMax && a->Tq * group <= 0x7fffffffLL;
+}
+
+template <int HD>
+int rows_pieces() { return AttnRowsCfg<HD>::PER_SM * current_sms(); }
+
+size_t rows_workspace(int head_dim) {
+  const size_t rows = 16 * 2 * static_cast<size_t>(head_dim == 64 ? rows_pieces<64>() : rows_pieces<128>());
+  return rows * head_dim * sizeof(float) + rows * sizeof(float2);
+}
+
+template <typename T, int HD>
+cudaError_t launch_attn_rows(const CUtensorMap& k, const CUtensorMap& v, const AttnPackedParams& a, void* ws, int* st,
+                             cudaStream_t s) {
+  static std::atomic<uint64_t> attr_done{0};
+  constexpr int smem = AttnRowsCfg<HD>::SMEM_BYTES;
+  cudaError_t e = set_smem_attr_once(attn_rows_kernel<T, HD>, smem, attr_done);
+  if (e != cudaSuccess) return e;
+  const int pieces = rows_pieces<HD>();
+  AttnRowsParams p{a, static_cast<float*>(ws), nullptr};
+  p.part_ml = reinterpret_cast<float2*>(p.part_o + static_cast<size_t>(pieces) * 2 * 16 * HD);
+  e = launch_pdl(attn_rows_kernel<T, HD>, dim3(pieces), dim3(ATTR_THREADS), smem, s, k, v, p, st);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(attn_join_kernel<T, HD>, dim3(pieces - 1), dim3(128), 0, s, p, pieces, st);
+}
+
+vit_status check_attention(const vit_attn_packed* a) {
+  if (!a) return fail(VIT_E_INVALID_ARG, "arguments are NULL");
+  if (a->type != VIT_DT_BF16 && a->type != VIT_DT_F16) return fail(VIT_E_UNSUPPORTED, "heads must be bf16 or fp16");
+  if (a->head_dim != 64 && a->head_dim != 128) return fail(VIT_E_UNSUPPORTED, "head_dim must be 64 or 128");
+  if (a->n < 0 || a->Tq < 0 || a->Tk < 0 || a->Tq > 0x3fffffffLL || a->Tk > 0x3fffffffLL || a->heads_q < 1 ||
+      a->heads_k < 1 || a->heads_q % a->heads_k || a->heads_q > 65535)
+    return fail(VIT_E_SHAPE, "need n >= 0, 0 <= Tq, Tk < 2^30, heads_q (at most 65535) a multiple of heads_k >= 1");
+  return VIT_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -329,13 +370,17 @@ vit_status vit_op_rope(const vit_rope_tensor* q, const vit_rope_tensor* k, vit_d
   return VIT_OK;
 }
 
+vit_status vit_op_attention_packed_workspace(const vit_attn_packed* a, size_t* bytes) {
+  const vit_status st = check_attention(a);
+  if (st != VIT_OK) return st;
+  if (!bytes) return fail(VIT_E_INVALID_ARG, "bytes is NULL");
+  *bytes = takes_rows_kernel(a) ? rows_workspace(a->head_dim) : 0;
+  return VIT_OK;
+}
+
 vit_status vit_op_attention_packed(const vit_attn_packed* a, vit_stream_t stream) {
-  if (!a) return fail(VIT_E_INVALID_ARG, "arguments are NULL");
-  if (a->type != VIT_DT_BF16 && a->type != VIT_DT_F16) return fail(VIT_E_UNSUPPORTED, "heads must be bf16 or fp16");
-  if (a->head_dim != 64 && a->head_dim != 128) return fail(VIT_E_UNSUPPORTED, "head_dim must be 64 or 128");
-  if (a->n < 0 || a->Tq < 0 || a->Tk < 0 || a->Tq > 0x3fffffffLL || a->Tk > 0x3fffffffLL || a->heads_q < 1 ||
-      a->heads_k < 1 || a->heads_q % a->heads_k || a->heads_q > 65535)
-    return fail(VIT_E_SHAPE, "need n >= 0, 0 <= Tq, Tk < 2^30, heads_q (at most 65535) a multiple of heads_k >= 1");
+  const vit_status st = check_attention(a);
+  if (st != VIT_OK) return st;
   if (!(a->scale > 0.f) || !std::isfinite(a->scale)) return fail(VIT_E_INVALID_ARG, "scale must be positive and finite");
   if (a->n == 0 || a->Tq == 0) return VIT_OK;
   if (!a->q || !a->out || !a->cu_q || !a->cu_k || (a->Tk > 0 && (!a->k || !a->v)))
@@ -347,6 +392,9 @@ vit_status vit_op_attention_packed(const vit_attn_packed* a, vit_stream_t stream
   for (int64_t s : strides)
     if (s % 8 || s < 0 || s >= (1LL << 38)) return fail(VIT_E_SHAPE, "strides must be multiples of 8, not negative");
   if (static_cast<int64_t>(a->n) + a->Tq / ATT_BM > 0x7fffffffLL) return fail(VIT_E_SHAPE, "too many sequences");
+  const bool rows = takes_rows_kernel(a);
+  if (rows && (!a->workspace || !aligned16(a->workspace) || a->workspace_bytes < rows_workspace(a->head_dim)))
+    return fail(VIT_E_WORKSPACE, "workspace missing, not 16-byte aligned or too small");
   AttnPackedParams p{};
   p.q = a->q;
   p.k = a->k;
@@ -376,12 +424,22 @@ vit_status vit_op_attention_packed(const vit_attn_packed* a, vit_stream_t stream
   const void* kb = a->Tk > 0 ? a->k : a->q;
   const void* vb = a->Tk > 0 ? a->v : a->q;
   const int64_t tkeys = std::max<int64_t>(1, a->Tk);
-  if (!tmap_heads(&tq, a->q, a->head_dim, a->heads_q, a->Tq, a->q_head, a->q_token, ATT_BM) ||
+  if ((!rows && !tmap_heads(&tq, a->q, a->head_dim, a->heads_q, a->Tq, a->q_head, a->q_token, ATT_BM)) ||
       !tmap_heads(&tk, kb, a->head_dim, a->heads_k, tkeys, a->k_head, a->k_token, 64) ||
       !tmap_heads(&tv, vb, a->head_dim, a->heads_k, tkeys, a->v_head, a->v_token, 64))
     return no_map();
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
+  if (rows) {
+    if (a->type == VIT_DT_BF16)
+      e = a->head_dim == 64 ? launch_attn_rows<__nv_bfloat16, 64>(tk, tv, p, a->workspace, a->status, s)
+                            : launch_attn_rows<__nv_bfloat16, 128>(tk, tv, p, a->workspace, a->status, s);
+    else
+      e = a->head_dim == 64 ? launch_attn_rows<__half, 64>(tk, tv, p, a->workspace, a->status, s)
+                            : launch_attn_rows<__half, 128>(tk, tv, p, a->workspace, a->status, s);
+    CK(e);
+    return VIT_OK;
+  }
   if (a->type == VIT_DT_BF16)
     e = a->head_dim == 64 ? launch_attn_packed<__nv_bfloat16, 64>(tq, tk, tv, p, a->status, s)
                           : launch_attn_packed<__nv_bfloat16, 128>(tq, tk, tv, p, a->status, s);

@@ -34,7 +34,7 @@ class VitAttnPacked(ctypes.Structure):
                 ("n", ctypes.c_int32), ("heads_q", ctypes.c_int32), ("heads_k", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32), ("type", ctypes.c_int32), ("causal", ctypes.c_int32),
                 ("max_q", ctypes.c_int32), ("scale", ctypes.c_float), ("status", ctypes.c_void_p),
-                ("wait_ns", ctypes.c_uint64)]
+                ("wait_ns", ctypes.c_uint64), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
 
 
 _fns = None
@@ -54,6 +54,7 @@ def _setup():
         "vit_op_rope_freqs": [F64, I32, I32, I32, F64, F64, F64, F64, P],
         "vit_op_rope": [ctypes.POINTER(VitRopeTensor), ctypes.POINTER(VitRopeTensor), I32, I64, I32, I32, P, I32, I32, P,
                         I32, F32, I32, P],
+        "vit_op_attention_packed_workspace": [ctypes.POINTER(VitAttnPacked), ctypes.POINTER(ctypes.c_size_t)],
         "vit_op_attention_packed": [ctypes.POINTER(VitAttnPacked), P],
         "vit_op_poll": [P],
     }
@@ -360,7 +361,12 @@ def attention_packed(q, k, v, cu_q, cu_k, len_k=None, causal: bool = False, scal
             q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), qt, qh, kt, kh, vt, vh, ot, oh, cu_q.data_ptr(),
             cu_k.data_ptr(), None if len_k is None else len_k.data_ptr(), Tq, Tk, n, Hq, Hk, d, _type_of(fn, q),
             1 if causal else 0, max_q, (1.0 / math.sqrt(d) if d else 0.0) if scale is None else scale,
-            None if status is None else status.data_ptr(), wait_ns)
+            None if status is None else status.data_ptr(), wait_ns, None, 0)
+        need = ctypes.c_size_t()
+        _check("vit_op_attention_packed_workspace", _fn("attention_packed_workspace")(args, need))
+        if need.value:
+            ws = torch.empty(need.value, dtype=torch.uint8, device=q.device)
+            args.workspace, args.workspace_bytes = ws.data_ptr(), need.value
         _check("vit_op_attention_packed", _fn(fn)(args, at.handle))
     return out
 
