@@ -34,16 +34,31 @@ struct AttnRowsCfg {
   static constexpr int K_BYTES = 64 * HD * 2;
   static constexpr int Q_BYTES = 16 * HD * 2;
   static constexpr int STAGE = 2 * K_BYTES + Q_BYTES;  // K | V | Q
-  static constexpr int STAGES = HD == 64 ? 6 : 3;
+  static constexpr int STAGES = HD == 64 ? 4 : 3;
   static constexpr int OFF_BAR = STAGES * STAGE;
-  static constexpr int SMEM_BYTES = OFF_BAR + 1024;
-  static constexpr int PER_SM = 2;
-  static_assert(SMEM_BYTES <= 115712, "two CTAs per SM");
+  static constexpr int SMEM_BYTES = OFF_BAR + 1536;
+  static constexpr int PER_SM = HD == 64 ? 3 : 2;
+  static_assert(PER_SM * (SMEM_BYTES + 1024) <= 233472, "CTAs per SM");
 };
+
+// Division by a number known at launch: n / d for 0 <= n < 2^31 (multiply by ceil(2^(32+l) / d) - 2^32 with
+// l = ceil(log2 d), of which n is the part the multiplier's 33rd bit adds).
+struct FastDiv {
+  uint32_t d, mul, shift;
+};
+inline FastDiv fast_div(uint32_t d) {
+  uint32_t l = 0;
+  while ((1ull << l) < d) ++l;
+  return {d, static_cast<uint32_t>(((1ull << 32) * ((1ull << l) - d)) / d + 1), l};
+}
+__device__ __forceinline__ int div_by(int n, const FastDiv& f) {
+  return static_cast<int>((__umulhi(static_cast<uint32_t>(n), f.mul) + static_cast<uint32_t>(n)) >> f.shift);
+}
 
 // Workspace: outputs [2 * CTAs][16][HD], then (maximum, sum) [2 * CTAs][16].
 struct AttnRowsParams {
   AttnPackedParams a;
+  FastDiv group;  // query heads a key head
   float* part_o;
   float2* part_ml;
 };
@@ -60,41 +75,59 @@ __device__ __forceinline__ void rows_shape(const SeqTile& s, int group, long lon
   nb = max(1, (s.lk + 63) / 64);
 }
 
-// One warp adds up the units of all sequences.  With want < 0 it returns their number; otherwise it
-// finds the sequence (seq, base: the sequence's first unit) that holds unit `want`.
-__device__ __forceinline__ long long rows_scan(const AttnPackedParams& p, long long want, int& seq, long long& base) {
+// One warp adds up the units of all sequences, 128 a round (four a lane).  pick(total) names the unit that
+// is looked for (< 0 or >= total: none); seq, base: the sequence that holds it (p.n: none) and that one's
+// first unit.  Up to 128 sequences are read once, more of them twice.
+template <typename F>
+__device__ __forceinline__ void rows_scan(const AttnPackedParams& p, int group, F pick, int& seq, long long& base) {
   const int lane = threadIdx.x & 31;
-  const int group = p.Hq / p.Hkv;
-  long long before = 0;
-  seq = p.n;
-  base = 0;
-  for (int at = 0; at < p.n; at += 32) {
-    long long mine = 0;
-    if (at + lane < p.n) {
-      SeqTile s;
-      seq_bounds(p, at + lane, s);
-      long long nt;
-      int nb;
-      rows_shape(s, group, nt, nb);
-      mine = nt * nb * p.Hkv;
+  long long cost[4], sum = 0, incl = 0, total = 0, before = 0;
+  auto round = [&](int at) {
+    sum = 0;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      cost[u] = 0;
+      if (at + lane * 4 + u < p.n) {
+        SeqTile s;
+        seq_bounds(p, at + lane * 4 + u, s);
+        long long nt;
+        int nb;
+        rows_shape(s, group, nt, nb);
+        cost[u] = nt * nb * p.Hkv;
+      }
+      sum += cost[u];
     }
-    long long incl = mine;
+    incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long up = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += up;
     }
-    const long long total = __shfl_sync(0xffffffffu, incl, 31);
-    if (want >= 0 && seq == p.n && want < before + total) {
-      const unsigned who = __ballot_sync(0xffffffffu, want < before + incl);
-      const int src = __ffs(static_cast<int>(who)) - 1;
-      seq = at + src;
-      base = before + __shfl_sync(0xffffffffu, incl - mine, src);
-      return 0;
+    return __shfl_sync(0xffffffffu, incl, 31);
+  };
+  for (int at = 0; at < p.n; at += 128) total += round(at);
+  const long long want = pick(total);
+  seq = p.n;
+  base = 0;
+  if (want < 0 || want >= total) return;
+  for (int at = 0; at < p.n; at += 128) {
+    const long long here = p.n <= 128 ? total : round(at);
+    if (want < before + here) {
+      const int src = __ffs(static_cast<int>(__ballot_sync(0xffffffffu, want < before + incl))) - 1;
+      base = before + __shfl_sync(0xffffffffu, incl - sum, src);
+      seq = at + src * 4;
+#pragma unroll
+      for (int u = 0; u < 3; ++u) {
+        const long long c = __shfl_sync(0xffffffffu, cost[u], src);
+        if (seq == at + src * 4 + u && want >= base + c) {
+          base += c;
+          ++seq;
+        }
+      }
+      return;
     }
-    before += total;
+    before += here;
   }
-  return before;
 }
 
 template <typename T>
@@ -135,7 +168,7 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
 __device__ __forceinline__ float to_max(float m, float top, float c) { return m == top ? 1.f : ex2_approx((m - top) * c); }
 
 template <typename T, int HD>
-__global__ void __launch_bounds__(ATTR_THREADS, 2)
+__global__ void __launch_bounds__(ATTR_THREADS, AttnRowsCfg<HD>::PER_SM)
     attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                      const __grid_constant__ AttnRowsParams pr, int* status) {
   using Cfg = AttnRowsCfg<HD>;
@@ -153,12 +186,12 @@ __global__ void __launch_bounds__(ATTR_THREADS, 2)
   uint64_t* empty = full + STAGES;
   uint64_t* join = empty + STAGES;  // the consumer warps' meeting point (bounded, unlike a barrier instruction)
   AttnRowsStage* desc = reinterpret_cast<AttnRowsStage*>(smem + Cfg::OFF_BAR + 128);  // [STAGES]
-  float2* s_ml = reinterpret_cast<float2*>(smem + Cfg::OFF_BAR + 384);                // [4][16]
+  float2* s_ml0 = reinterpret_cast<float2*>(smem + Cfg::OFF_BAR + 384);               // [2][4][16]
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::OFF_BAR + 112);
   int* s_count = reinterpret_cast<int*>(smem + Cfg::OFF_BAR + 116);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int group = p.Hq / p.Hkv;
+  const int group = static_cast<int>(pr.group.d);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -175,11 +208,12 @@ __global__ void __launch_bounds__(ATTR_THREADS, 2)
   long long u = 0, u_end = 0, base = 0, per = 0;
   int seq = 0;
   if (warp == 4) {
-    const long long total = rows_scan(p, -1, seq, base);
-    per = max(static_cast<long long>(ATTR_MIN_UNITS), (total + gridDim.x - 1) / gridDim.x);
-    u = min(total, per * blockIdx.x);
-    u_end = min(total, u + per);
-    if (u < u_end) rows_scan(p, u, seq, base);
+    rows_scan(p, group, [&](long long total) {
+      per = max(static_cast<long long>(ATTR_MIN_UNITS), (total + gridDim.x - 1) / gridDim.x);
+      u = min(total, per * blockIdx.x);
+      u_end = min(total, u + per);
+      return u;
+    }, seq, base);
     if (lane == 0) *s_count = static_cast<int>(min(u_end - u, 0x7fffffffLL));
   }
   pdl_launch_dependents();
@@ -201,22 +235,23 @@ __global__ void __launch_bounds__(ATTR_THREADS, 2)
       int nb = 1;
       seq_bounds(p, seq, s);
       rows_shape(s, group, nt, nb);
+      // the first item of the piece; from there on they are counted up
+      const long long item = (u - base) / nb;
+      int blk = static_cast<int>(u - base - item * nb);
+      int hk = static_cast<int>(item / nt);
+      int tile = static_cast<int>(item - hk * nt);
       while (ok && u < u_end) {
-        long long rem = u - base;
-        while (rem >= nt * nb * p.Hkv && seq + 1 < p.n) {  // the next sequence that has rows
-          base += nt * nb * p.Hkv;
-          rem = u - base;
-          seq_bounds(p, ++seq, s);
+        if (hk == p.Hkv) {  // the next sequence that has rows
+          hk = 0;
+          do seq_bounds(p, ++seq, s);
+          while (s.lq == 0 && seq + 1 < p.n);
           rows_shape(s, group, nt, nb);
         }
-        const long long item = rem / nb;
-        const int blk = static_cast<int>(rem - item * nb);
-        const int hk = static_cast<int>(item / nt);
-        const int row0 = static_cast<int>(item - hk * nt) * 16;
+        const int row0 = tile * 16;
         const int take = static_cast<int>(min(static_cast<long long>(nb - blk), u_end - u));
         const int rows = s.lq * group;
         const int off = s.lk - s.lq;
-        const int kend = p.causal ? clampi(min(row0 + 15, rows - 1) / group + off + 1, 0, s.lk) : s.lk;
+        const int kend = p.causal ? clampi(div_by(min(row0 + 15, rows - 1), pr.group) + off + 1, 0, s.lk) : s.lk;
         const int part = (blk > 0 || take < nb) ? (ATTR_PART | (u == start ? 0 : ATTR_ODD)) : 0;
         for (int b = 0; b < take; ++b) {
           if (!mbar_wait_warp(&empty[slot], ph ^ 1u, abort_flag, gstatus, DEV_TIMEOUT_ATTR + 1, p.wait_ns)) {
@@ -229,7 +264,7 @@ __global__ void __launch_bounds__(ATTR_THREADS, 2)
             for (int i = lane; i < 16 * (HD / 8); i += 32) {
               const int r = i / (HD / 8), c = i % (HD / 8);
               const int row = min(row0 + r, rows - 1);
-              const int t = row / group;
+              const int t = div_by(row, pr.group);
               const void* src = static_cast<const T*>(p.q) + static_cast<int64_t>(s.q0 + t) * p.q_tok +
                                 static_cast<int64_t>(hk * group + row - t * group) * p.q_head + c * 8;
               asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(st + 2 * Cfg::K_BYTES) + swz(r, c, 16)),
@@ -270,6 +305,11 @@ __global__ void __launch_bounds__(ATTR_THREADS, 2)
           }
         }
         u += take;
+        blk = 0;
+        if (++tile == nt) {
+          tile = 0;
+          ++hk;
+        }
       }
       if (*abort_flag) {
         for (int i = 0; i < STAGES; ++i)
@@ -285,6 +325,7 @@ __global__ void __launch_bounds__(ATTR_THREADS, 2)
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
     int slot = 0;
     uint32_t ph = 0, jp = 0;
+    int s_flip = 0;  // two sets of s_ml: a warp that is done may begin the next item's
     auto meet = [&]() {
       __syncwarp();
       if (lane == 0) mbar_arrive(join);
@@ -311,7 +352,7 @@ __global__ void __launch_bounds__(ATTR_THREADS, 2)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const int row = min(d.row0 + g + 8 * r, d.rows - 1);
-        lim[r] = (p.causal ? min(d.lk, row / group + d.off + 1) : d.lk) - key;
+        lim[r] = (p.causal ? min(d.lk, div_by(row, pr.group) + d.off + 1) : d.lk) - key;
       }
       if (__any_sync(0xffffffffu, lim[1] > 0 || lim[0] > 0)) {
         float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
@@ -380,6 +421,7 @@ __global__ void __launch_bounds__(ATTR_THREADS, 2)
       }
       if (d.flags & ATTR_LAST) {
         // join the four warps through the stage's K and V, which all have read by then
+        float2* s_ml = s_ml0 + s_flip * 64;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
@@ -410,7 +452,7 @@ __global__ void __launch_bounds__(ATTR_THREADS, 2)
           for (int x = 1; x < 4; ++x) top = maxn(top, s_ml[x * 16 + row].x);
 #pragma unroll
           for (int x = 0; x < 4; ++x) sum += s_ml[x * 16 + row].y * to_max(s_ml[x * 16 + row].x, top, c);
-          const int t = arow / group;
+          const int t = div_by(arow, pr.group);
           const bool sees = (p.causal ? min(d.lk, t + d.off + 1) : d.lk) > 0;
           const float inv = sees ? 1.0f / sum : 0.f;
           T* dst = static_cast<T*>(p.out) + static_cast<int64_t>(d.q0 + t) * p.o_tok +
@@ -451,7 +493,7 @@ __global__ void __launch_bounds__(ATTR_THREADS, 2)
             pr.part_ml[static_cast<int64_t>(cta_slot) * 16 + row] = make_float2(top, sum);
         }
         fence_proxy_async_smem();  // the stage was written here; the next write is a copy's
-        if (!meet()) break;  // s_ml and the stage are free
+        s_flip ^= 1;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[slot]);
@@ -470,18 +512,15 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ 
   const AttnPackedParams& p = pr.a;
   __shared__ long long s_at[4];
   __shared__ int s_seq;
-  const int group = p.Hq / p.Hkv;
+  const int group = static_cast<int>(pr.group.d);
   // the lengths were there before the kernel ahead began: only its results have to be waited for
   if (threadIdx.x < 32) {
-    int seq = 0;
-    long long base = 0;
-    const long long total = rows_scan(p, -1, seq, base);
-    const long long per = max(static_cast<long long>(ATTR_MIN_UNITS), (total + pieces - 1) / pieces);
-    const long long at = per * (blockIdx.x + 1);
-    if (at < total)
-      rows_scan(p, at, seq, base);
-    else
-      seq = p.n;
+    int seq;
+    long long base, per = 0, at = 0;
+    rows_scan(p, group, [&](long long total) {
+      per = max(static_cast<long long>(ATTR_MIN_UNITS), (total + pieces - 1) / pieces);
+      return at = per * (blockIdx.x + 1);
+    }, seq, base);
     if (threadIdx.x == 0) {
       s_seq = seq;
       s_at[0] = at;
@@ -530,7 +569,7 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ 
       v.z += a.z * w;
       v.w += a.w * w;
     }
-    const int t = arow / group;
+    const int t = div_by(arow, pr.group);
     const bool sees = (p.causal ? min(s.lk, t + off + 1) : s.lk) > 0;
     const float inv = sees ? 1.0f / sum : 0.f;
     T* dst = static_cast<T*>(p.out) + static_cast<int64_t>(s.q0 + t) * p.o_tok +

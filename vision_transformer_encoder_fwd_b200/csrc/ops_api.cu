@@ -190,17 +190,20 @@ size_t rows_workspace(int head_dim) {
 }
 
 template <typename T, int HD>
-cudaError_t launch_attn_rows(const CUtensorMap& k, const CUtensorMap& v, const AttnPackedParams& a, void* ws, int* st,
-                             cudaStream_t s) {
+cudaError_t launch_attn_rows(const CUtensorMap& k, const CUtensorMap& v, const AttnPackedParams& a, int max_q, void* ws,
+                             int* st, cudaStream_t s) {
   static std::atomic<uint64_t> attr_done{0};
   constexpr int smem = AttnRowsCfg<HD>::SMEM_BYTES;
   cudaError_t e = set_smem_attr_once(attn_rows_kernel<T, HD>, smem, attr_done);
   if (e != cudaSuccess) return e;
-  const int pieces = rows_pieces<HD>();
-  AttnRowsParams p{a, static_cast<float*>(ws), nullptr};
+  AttnRowsParams p{a, fast_div(static_cast<uint32_t>(a.Hq / a.Hkv)), static_cast<float*>(ws), nullptr};
+  // no more pieces than there can be work for, by the row tiles that max_q promises (any number is right)
+  const int64_t tiles = (static_cast<int64_t>(max_q) * p.group.d + 15) / 16;
+  const int64_t units = a.Hkv * tiles * (a.Tk / 64 + a.n);
+  const int pieces = static_cast<int>(std::min<int64_t>(rows_pieces<HD>(), (units + ATTR_MIN_UNITS - 1) / ATTR_MIN_UNITS));
   p.part_ml = reinterpret_cast<float2*>(p.part_o + static_cast<size_t>(pieces) * 2 * 16 * HD);
   e = launch_pdl(attn_rows_kernel<T, HD>, dim3(pieces), dim3(ATTR_THREADS), smem, s, k, v, p, st);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || pieces == 1) return e;
   return launch_pdl(attn_join_kernel<T, HD>, dim3(pieces - 1), dim3(128), 0, s, p, pieces, st);
 }
 
@@ -432,11 +435,11 @@ vit_status vit_op_attention_packed(const vit_attn_packed* a, vit_stream_t stream
   cudaError_t e;
   if (rows) {
     if (a->type == VIT_DT_BF16)
-      e = a->head_dim == 64 ? launch_attn_rows<__nv_bfloat16, 64>(tk, tv, p, a->workspace, a->status, s)
-                            : launch_attn_rows<__nv_bfloat16, 128>(tk, tv, p, a->workspace, a->status, s);
+      e = a->head_dim == 64 ? launch_attn_rows<__nv_bfloat16, 64>(tk, tv, p, a->max_q, a->workspace, a->status, s)
+                            : launch_attn_rows<__nv_bfloat16, 128>(tk, tv, p, a->max_q, a->workspace, a->status, s);
     else
-      e = a->head_dim == 64 ? launch_attn_rows<__half, 64>(tk, tv, p, a->workspace, a->status, s)
-                            : launch_attn_rows<__half, 128>(tk, tv, p, a->workspace, a->status, s);
+      e = a->head_dim == 64 ? launch_attn_rows<__half, 64>(tk, tv, p, a->max_q, a->workspace, a->status, s)
+                            : launch_attn_rows<__half, 128>(tk, tv, p, a->max_q, a->workspace, a->status, s);
     CK(e);
     return VIT_OK;
   }
