@@ -7,6 +7,9 @@ operators; each includes its kernel headers), compiled side by side.  It links t
 statically and resolves the driver's tensor-map encoder at run time, so it needs no libcuda at
 link time and cross-compiles on a machine without a GPU.  The objects stay in _build/ and are
 kept while none of the files that went into them has changed.
+
+csrc/ops_bind.cpp becomes _vit_ops.so, the operators' binding: an extension module against torch's
+headers that calls the library next to it.
 """
 from __future__ import annotations
 
@@ -22,6 +25,7 @@ ROOT = os.path.dirname(PKG_DIR)
 CSRC = os.path.join(PKG_DIR, "csrc")
 LIB_NAME = "libvit_b200.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
+BIND_PATH = os.path.join(PKG_DIR, "_vit_ops.so")
 OBJ_DIR = os.path.join(PKG_DIR, "_build")
 ARCH_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
@@ -35,12 +39,12 @@ def _nvcc() -> str:
 
 def _sources():
     deps = sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cuh")) +
-                  glob.glob(os.path.join(ROOT, "include", "*.h")))
+                  glob.glob(os.path.join(CSRC, "*.cpp")) + glob.glob(os.path.join(ROOT, "include", "*.h")))
     return [os.path.join(CSRC, "vit_api.cu"), os.path.join(CSRC, "ops_api.cu")], deps
 
 
 def _object_current(obj: str) -> bool:
-    """Whether `obj` is newer than every file its dependency list (written by nvcc) names."""
+    """Whether `obj` is newer than every file its dependency list (written by the compiler) names."""
     try:
         with open(obj + ".d") as f:
             names = f.read().replace("\\\n", " ").split(":", 1)[1].split()
@@ -51,10 +55,30 @@ def _object_current(obj: str) -> bool:
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not (os.path.exists(LIB_PATH) and os.path.exists(BIND_PATH)):
         return False
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(BIND_PATH))
     return all(os.path.getmtime(d) <= t for d in _sources()[1])
+
+
+def _bind_commands(obj: str):
+    """Compile and link commands of the operators' binding."""
+    import sysconfig
+
+    import torch
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    inc = ["-I" + sysconfig.get_paths()["include"]]
+    for d in (os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
+              os.path.join(cuda, "include")):
+        inc += ["-isystem", d]
+    libs = os.path.join(base, "lib")
+    cc = os.environ.get("CXX") or "g++"
+    abi = f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"
+    return ([cc, "-O2", "-fPIC", "-std=c++20", abi, *inc, "-MMD", "-MF", obj + ".d", "-c", "-o", obj,
+             os.path.join(CSRC, "ops_bind.cpp")],
+            [cc, "-shared", "-o", BIND_PATH + ".tmp", obj, "-L" + libs, "-L" + PKG_DIR, "-ltorch_python", "-ltorch_cpu",
+             "-ltorch", "-lc10", "-lc10_cuda", "-l:" + LIB_NAME, "-Wl,-rpath,$ORIGIN"])
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
@@ -72,6 +96,10 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
         if force or verbose_ptxas or not _object_current(obj):
             cmd = [_nvcc(), *flags, "-MMD", "-MF", obj + ".d", "-c", "-o", obj, src]
             running.append(subprocess.Popen(cmd, cwd=ROOT, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True))
+    bind = os.path.join(OBJ_DIR, "ops_bind.o")
+    bind_compile, bind_link = _bind_commands(bind)
+    if force or not _object_current(bind):
+        running.append(subprocess.Popen(bind_compile, cwd=ROOT, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True))
     said = [(p.communicate()[0], p.returncode) for p in running]
     tmp = LIB_PATH + ".tmp"
     if all(rc == 0 for _, rc in said):
@@ -82,8 +110,13 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     if bad or verbose_ptxas:
         sys.stderr.write("".join(text for text, _ in said))
     if bad:
-        raise RuntimeError(f"nvcc failed with exit code {bad[0]}")
+        raise RuntimeError(f"a compiler failed with exit code {bad[0]}")
     os.replace(tmp, LIB_PATH)
+    p = subprocess.run(bind_link, cwd=ROOT, capture_output=True, text=True)
+    if p.returncode != 0:
+        sys.stderr.write(p.stdout + p.stderr)
+        raise RuntimeError(f"linking the operators' binding failed with exit code {p.returncode}")
+    os.replace(BIND_PATH + ".tmp", BIND_PATH)
     return LIB_PATH
 
 
