@@ -700,3 +700,34 @@ def test_attention_rows_wait_expiry_is_reported(d):
     V.attention_packed(q, k, v, cu_q, cu_k, max_q=1, out=out)
     V.op_poll()
     check_attn(out, q, k, v, list(range(n)), cu_k.tolist(), [1] * n, [lk] * n, False, d ** -0.5)
+
+
+@pytest.mark.parametrize("M,N,K", [(17, 4096, 4096), (33, 4096, 2064), (100, 1000, 4096), (128, 72, 8192), (129, 2056, 1008),
+                                   (257, 640, 2048), (1000, 1024, 1024), (1024, 4096, 4096), (4096, 1024, 1024), (255, 8, 160)])
+def test_linear_fp8_by_every_kernel(M, N, K):
+    """Sizes on both sides of the choices between the kernels; rows and columns past the ends are left."""
+    V = lib()
+    a, sa, w, sw, b = make_linear(M, N, K, M + K, True)
+    big = torch.full((M + 3, N + 8), 7.0, device="cuda", dtype=torch.bfloat16)
+    V.linear_fp8(a, sa, w, sw, bias=b, out=big[:M, :N])
+    V.op_poll()
+    check_linear(big[:M, :N], a, sa, w, sw, b)
+    assert (big[M:] == 7).all() and (big[:, N:] == 7).all()
+    again = V.linear_fp8(a, sa, w, sw, bias=b)
+    assert torch.equal(again, big[:M, :N])
+
+
+@pytest.mark.parametrize("M,N,K", [(200, 1024, 4096), (3000, 512, 8192)])
+def test_linear_split_and_tile_wait_expiry_is_reported(M, N, K):
+    V = lib()
+    a, sa, w, sw, b = make_linear(M, N, K, 25, True)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    V.linear_fp8(a, sa, w, sw, status=st, wait_ns=200)
+    torch.cuda.synchronize()
+    assert 0x300 < int(st.item()) < 0x400
+    out = torch.full((M, N), 7.0, device="cuda", dtype=torch.bfloat16)
+    V.linear_fp8(a, sa, w, sw, status=st, out=out)
+    assert (out == 7).all()
+    V.linear_fp8(a, sa, w, sw, bias=b, out=out)
+    V.op_poll()
+    check_linear(out, a, sa, w, sw, b)

@@ -148,16 +148,78 @@ bool tmap_heads(CUtensorMap* tm, const void* base, int d, int heads, int64_t tok
 vit_status no_map() { return fail(VIT_E_CUDA, "cuTensorMapEncodeTiled refused a tensor map"); }
 
 // ------------------------------------------------------------------ linear
-template <int BN>
-cudaError_t launch_lin8(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o, const Lin8Params& p, int* st,
-                        cudaStream_t s, int nsm) {
+cudaError_t launch_lin8_tile(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o, const Lin8Params& p, int* st,
+                             cudaStream_t s, int nsm) {
   static std::atomic<uint64_t> attr_done{0};
-  constexpr int smem = Lin8Cfg<BN>::SMEM_BYTES;
-  cudaError_t e = set_smem_attr_once(lin8_tile_kernel<BN>, smem, attr_done);
+  cudaError_t e = set_smem_attr_once(lin8_tile_kernel, Lin8Cfg::SMEM_BYTES, attr_done);
   if (e != cudaSuccess) return e;
-  const long long tiles = static_cast<long long>((p.M + LIN8_BM - 1) / LIN8_BM) * ((p.N + BN - 1) / BN);
-  return launch_pdl(lin8_tile_kernel<BN>, dim3(static_cast<unsigned>(std::min<long long>(tiles, nsm))),
-                    dim3(LIN8_THREADS), smem, s, a, b, o, p, st);
+  const long long tiles = static_cast<long long>((p.M + 127) / 128) * ((p.N + 127) / 128);
+  return launch_pdl(lin8_tile_kernel, dim3(static_cast<unsigned>(std::min<long long>(tiles, nsm))), dim3(LIN8_THREADS),
+                    Lin8Cfg::SMEM_BYTES, s, a, b, o, p, st);
+}
+
+cudaError_t launch_lin8_pair(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o, const Lin8Params& p, int* st,
+                             cudaStream_t s, int nsm) {
+  static std::atomic<uint64_t> attr_done{0};
+  static std::atomic<int> max_clusters{0};
+  constexpr int smem = Lin8PairCfg::SMEM_BYTES;
+  cudaError_t e = set_smem_attr_once(lin8_pair_kernel, smem, attr_done);
+  if (e != cudaSuccess) return e;
+  int mc = max_clusters.load();
+  if (mc == 0) {
+    // how many 2-CTA clusters fit on the device at once (an SM can be left without a partner)
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * (nsm / 2));
+    cfg.blockDim = dim3(LIN8_THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, lin8_pair_kernel, &cfg) != cudaSuccess || n < 1) {
+      cudaGetLastError();
+      n = nsm / 2;
+    }
+    mc = std::max(1, std::min(n, nsm / 2));
+    max_clusters.store(mc);
+  }
+  const long long tiles = static_cast<long long>((p.M + 255) / 256) * ((p.N + 255) / 256);
+  return launch_pdl(lin8_pair_kernel, dim3(static_cast<unsigned>(2 * std::min<long long>(tiles, mc))), dim3(LIN8_THREADS), smem,
+                    s, a, b, o, p, st);
+}
+
+template <int SPLITS>
+cudaError_t launch_lin8_split(const CUtensorMap& a, const CUtensorMap& b, const Lin8Params& p, __nv_bfloat16* out,
+                              int64_t ldo, int* st, cudaStream_t s) {
+  static std::atomic<uint64_t> attr_done{0};
+  cudaError_t e = set_smem_attr_once(lin8_split_kernel<SPLITS>, Lin8SplitCfg::SMEM_BYTES, attr_done);
+  if (e != cudaSuccess) return e;
+  const long long tiles = static_cast<long long>((p.M + 127) / 128) * ((p.N + 127) / 128);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles * SPLITS));
+  cfg.blockDim = dim3(LIN8_THREADS);
+  cfg.dynamicSmemBytes = Lin8SplitCfg::SMEM_BYTES;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = SPLITS;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl_enabled() ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, lin8_split_kernel<SPLITS>, a, b, p, out, ldo, st);
+}
+
+template <int NB>
+cudaError_t launch_lin8_rows(const Lin8RowsParams& r, int* st, cudaStream_t s) {
+  return launch_pdl(lin8_rows_kernel<NB>, dim3((r.p.N + 15) / 16), dim3(32 * LIN8R_WARPS), 0, s, r, st);
 }
 
 // ------------------------------------------------------------------ attention
@@ -262,11 +324,43 @@ vit_status vit_op_linear_fp8(const void* A, int64_t lda, const float* a_scales, 
     return fail(VIT_E_SHAPE, "leading dimensions: at least a row, lda and ldw multiples of 16, ldo of 8");
   const int nsm = current_sms();
   Lin8Params p{M, N, K, a_scales, w_scales, bias, wait_ns};
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  // Measured on a B200 (148 SMs), us with the weights in L2, row kernel against K split over clusters:
+  // M = 16, N = 6144, K = 4096: 7.9 / 12.3; M = 32: 512 x 1024 3.1 / 4.9, 1024 x 4096 5.2 / 6.4, 4096 x 4096
+  // 12.7 / 7.2 (every CTA of the row kernel reads all of A, which past 16 rows is most of its bytes).
+  if (M <= 16 || (M <= 32 && static_cast<long long>(N) * K <= 1 << 22)) {
+    const Lin8RowsParams r{p, static_cast<const uint8_t*>(A), static_cast<const uint8_t*>(W), static_cast<__nv_bfloat16*>(out),
+                           M > 1 ? lda : 0, N > 1 ? ldw : 0, M > 1 ? ldo : 0};
+    CK(M <= 8 ? launch_lin8_rows<1>(r, status, s) : M <= 16 ? launch_lin8_rows<2>(r, status, s)
+                                                            : launch_lin8_rows<4>(r, status, s));
+    return VIT_OK;
+  }
   CUtensorMap ta, tb, to;
   if (!tmap_rows8(&ta, A, K, M, std::max<int64_t>(lda, K), LIN8_BM) ||
       !tmap_rows8(&tb, W, K, N, std::max<int64_t>(ldw, K), 128) || !tmap_out16(&to, out, N, M, std::max<int64_t>(ldo, N)))
     return no_map();
-  CK(launch_lin8<128>(ta, tb, to, p, status, reinterpret_cast<cudaStream_t>(stream), nsm));
+  const long long steps = (K + LIN8_BK - 1) / LIN8_BK;
+  const long long tiles = static_cast<long long>((M + 127) / 128) * ((N + 127) / 128);
+  // Few tiles: K over clusters, as long as a CTA keeps four steps.  Against one CTA a tile: 33 x 4096 x
+  // 4096 7.2 / 12.9 us, 100 x 1024 x 4096 9.2 / 12.9, 512 x 1024 x 4096 10.0 / 13.3; with two steps a CTA
+  // (256 x 1024 x 1024) 7.6 / 7.2.
+  int splits = tiles <= nsm / 10 ? 8 : tiles <= nsm / 4 ? 4 : tiles <= nsm / 2 ? 2 : 1;
+  while (splits > 1 && steps < 4 * splits) splits /= 2;
+  if (splits > 1) {
+    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out);
+    const int64_t ld = M > 1 ? ldo : 0;
+    CK(splits == 8 ? launch_lin8_split<8>(ta, tb, p, o, ld, status, s)
+                   : splits == 4 ? launch_lin8_split<4>(ta, tb, p, o, ld, status, s)
+                                 : launch_lin8_split<2>(ta, tb, p, o, ld, status, s));
+    return VIT_OK;
+  }
+  // A step of K takes 0.28 us of a 128 x 128 tile, 0.40 us of a 256 x 256 tile on two SMs, and the paired
+  // kernel 3 us more to start: 1024 x 4096 x 4096 24 us in small tiles, 20.6 paired; 4096^3 71 / 55; 2048 x
+  // 1024 x 4096 14.4 / 18.7.
+  auto waves = [](long long t, int at_once) { return (t + at_once - 1) / at_once; };
+  const long long pair_ns = 400 * steps * waves(static_cast<long long>((M + 255) / 256) * ((N + 255) / 256), nsm / 2) + 3000;
+  const long long tile_ns = 280 * steps * waves(tiles, nsm);
+  CK(pair_ns < tile_ns ? launch_lin8_pair(ta, tb, to, p, status, s, nsm) : launch_lin8_tile(ta, tb, to, p, status, s, nsm));
   return VIT_OK;
 }
 
