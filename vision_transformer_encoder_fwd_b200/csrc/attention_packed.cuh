@@ -6,15 +6,20 @@
 // 0 .. t + lk - lq (the last query sees the last key):
 //   out = sum_j softmax_j(scale q . k_j) v_j,    a row that sees nothing is 0.
 //
-// One CTA per (128-query tile, head), 6 warps, two CTAs per SM, in the design of the fixed-length
-// kernel (64-key sub-blocks, two S buffers in TMEM that they alternate between, P written over S,
-// the running maximum moved only when it grows by more than 2^8):
-//   warp 0      TMA: Q once, then K and V tiles of 64 keys in the order the MMAs use them
-//   warp 1      TMEM and the MMAs  S_b = Q K_n^T (both from shared memory), O += P_n V_n
-//   warps 2..5  softmax, one query row per thread
-// How it differs: Q stays in shared memory (at width 128 there is no TMEM left for it: two S buffers
-// and O fill the CTA's 256 columns), the row sums are kept in registers at width 128 and by
-// the MMA (a column of ones behind V) at width 64.
+// One CTA per (tile of 128 rows, group of heads), 6 warps.  A row is one query of one head: the heads
+// of a tile share a key head, `pack` of them side by side (row t * pack + g), so that short sequences
+// with grouped heads still fill a tile.
+//   warp 0      TMA: Q once, then K and V blocks of KEYS keys in the order the MMAs use them
+//   warp 1      TMEM and the MMAs  S = Q K_n^T (both from shared memory), O += P_n V_n
+//   warps 2..5  softmax, one row per thread; P is written over S
+// The keys are taken in blocks of 64 with two S buffers in tensor memory, so that the S of the next block
+// is there when a softmax ends; two CTAs per SM.  The softmax's exponentials (16 a clock and SM on the
+// special-function unit) bound it at width 64, the MMAs with them at width 128; what costs in practice
+// is the time from one block's P to the S two blocks on, most of it the issuing thread's own.  It is
+// chosen by elect.sync, which lets the compiler keep descriptors in uniform registers (four MMAs and
+// a commit take 135 clocks; 365 under an ordinary predicate), commits once per S and once per O (the
+// copies' slots are freed by the same barriers) and has K and V in hand before it waits for P.  The
+// running maximum moves only when it grows by more than 2^8.
 // What a tile reads past its sequence's last key belongs to somebody else or to nobody and may be
 // NaN: scores there are replaced before use, and V's rows there are overwritten with zeros in
 // shared memory, since 0 * NaN would reach every row of O.
@@ -42,11 +47,12 @@ struct AttnPackedParams {
   const int* cu_k;
   const int* len_k;  // or NULL
   int n, Tq, Tk, Hq, Hkv, causal;
+  int pack, tokens;  // tile kernel: heads and queries a tile
   float scale_log2;  // scale * log2(e)
   unsigned long long wait_ns;
 };
 
-// Where a tile of `bm` query rows lies: sequence bounds, all clamped to the buffers.
+// Where a tile of queries lies: sequence bounds, all clamped to the buffers.
 struct SeqTile {
   int q0, lq, k0, lk, tile, seq;
 };
@@ -61,10 +67,9 @@ __device__ __forceinline__ void seq_bounds(const AttnPackedParams& p, int i, Seq
   if (p.len_k != nullptr) s.lk = clampi(p.len_k[i], 0, s.lk);
 }
 
-// Finds tile number `want` in the order of the sequences, ceil(lq * mul / bm) tiles each (mul:
-// rows per query).  One warp; every lane gets the answer.  Each round takes 128 sequences, four
+// Finds tile number `want` in the order of the sequences, ceil(lq / bm) tiles each.  One warp; every lane gets the answer.  Each round takes 128 sequences, four
 // per lane, so that up to that many cost one trip to memory.  seq = -1: there is no such tile.
-__device__ __forceinline__ SeqTile find_tile(const AttnPackedParams& p, int want, int bm, int mul) {
+__device__ __forceinline__ SeqTile find_tile(const AttnPackedParams& p, int want, int bm) {
   const int lane = threadIdx.x & 31;
   SeqTile s;
   s.seq = -1;
@@ -76,7 +81,7 @@ __device__ __forceinline__ SeqTile find_tile(const AttnPackedParams& p, int want
     int cnt[4], sum = 0;
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      cnt[u] = (base + lane * 4 + u < p.n) ? (max(0, c[u + 1] - c[u]) * mul + bm - 1) / bm : 0;
+      cnt[u] = (base + lane * 4 + u < p.n) ? (max(0, c[u + 1] - c[u]) + bm - 1) / bm : 0;
       sum += cnt[u];
     }
     int incl = sum;
@@ -125,53 +130,95 @@ __host__ __device__ constexpr uint32_t idesc_of(int M, int N, bool b_mn_major) {
                                         : idesc_bf16(M, N, b_mn_major);
 }
 
-template <int HD>
-struct AttnPackedCfg {
-  static constexpr int UNIT = 64 * HD * 2;        // one K or V tile
-  static constexpr int UNITS = (HD == 64) ? 10 : 5;
-  static constexpr int Q_BYTES = 128 * HD * 2;
-  static constexpr int OFF_Q = 0;
-  static constexpr int OFF_RING = OFF_Q + Q_BYTES;
-  static constexpr int OFF_ONES = OFF_RING + UNITS * UNIT;  // width 64: the atom of ones behind V
-  static constexpr int OFF_BAR = OFF_ONES + (HD == 64 ? 8192 : 0);
-  static constexpr int SMEM_BYTES = OFF_BAR + 256;
-  static constexpr bool ONES = HD == 64;
-  static constexpr uint32_t TMEM_COLS = 256;
-  static constexpr int O_COLS = ONES ? 80 : HD;
-  static constexpr uint32_t TM_S = 0, TM_O = 128;
-  static_assert(SMEM_BYTES <= 115712, "two CTAs per SM");
-  static_assert(8 * (2 * UNITS + 7) + 8 + 4 * 8 <= 256, "barrier area");
-};
-
-// Maxima that keep a NaN: a score that is one has to reach its row's output, and the row maximum is
-// the way there (the FMA-pipe exponential would lose it).
+// Maximum that keeps a NaN.
 __device__ __forceinline__ float maxn(float a, float b) { return max_nan(a, b); }
-__device__ __forceinline__ float maxn(float a, float b, float c) {
-  float d;
-  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-__device__ __forceinline__ float row_maxn64(const float (&s)[64]) {
-  float m0 = maxn(s[0], s[1]), m1 = maxn(s[2], s[3]), m2 = maxn(s[4], s[5]), m3 = maxn(s[6], s[7]);
-#pragma unroll
-  for (int t = 8; t < 64; t += 8) {
-    m0 = maxn(m0, s[t], s[t + 1]);
-    m1 = maxn(m1, s[t + 2], s[t + 3]);
-    m2 = maxn(m2, s[t + 4], s[t + 5]);
-    m3 = maxn(m3, s[t + 6], s[t + 7]);
-  }
-  return maxn(m0, m1, maxn(m2, m3));
-}
 
 // m * c as the softmax's exponents subtract it: 0 for a row that has seen no key yet (its P are 0), NaN
 // for a maximum of +infinity, whose row has no softmax.
 __device__ __forceinline__ float max_offset(float m, float c) { return m == -INFINITY ? 0.f : fmaf(m, c, m - m); }
 
-// P for one row of a 64-key sub-block, as softmax_sub_p with a scale known at launch; returns the
-// sum of the unrounded values (used at width 128).
+// Factor that brings sums at maximum m to the common maximum top.
+__device__ __forceinline__ float to_max(float m, float top, float c) { return m == top ? 1.f : ex2_approx((m - top) * c); }
+
+// One thread of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e != 0;
+}
+// Bounded waits, by a whole warp or by one thread, whose slow part stays out of the loops that wait.
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* gstatus, int site,
+                                       unsigned long long limit) {
+  uint64_t* b = static_cast<uint64_t*>(__cvta_shared_to_generic(bar));
+  return mbar_wait_warp<32>(b, parity, abort_flag, gstatus, site, limit);
+}
+__device__ __noinline__ bool wait_one_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* gstatus, int site,
+                                           unsigned long long limit) {
+  return mbar_wait<32>(static_cast<uint64_t*>(__cvta_shared_to_generic(bar)), parity, abort_flag, gstatus, site, limit);
+}
+__device__ __forceinline__ bool test_bar(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(ok)
+               : "r"(bar), "r"(parity)
+               : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* gstatus, int site,
+                                          unsigned long long limit) {
+  if (__all_sync(0xffffffffu, test_bar(bar, parity))) return true;
+  return wait_slow(bar, parity, abort_flag, gstatus, site, limit);
+}
+__device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* gstatus, int site,
+                                         unsigned long long limit) {
+  return test_bar(bar, parity) || wait_one_slow(bar, parity, abort_flag, gstatus, site, limit);
+}
+
+template <int HD>
+struct AttnPackedCfg {
+  static constexpr int UNIT = 64 * HD * 2;  // a K or V tile of 64 keys, slabs of 64 values
+  static constexpr int UNITS = (HD == 64) ? 10 : 5;
+  static constexpr int PER_SM = 2;
+  static constexpr int Q_BYTES = 128 * HD * 2;
+  static constexpr bool ONES = HD == 64;  // row sums by the MMA: a column of ones behind V
+  static constexpr int O_COLS = ONES ? 80 : HD;
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_RING = OFF_Q + Q_BYTES;
+  static constexpr int OFF_ONES = OFF_RING + UNITS * UNIT;
+  static constexpr int OFF_BAR = OFF_ONES + (ONES ? 8192 : 0);
+  static constexpr int DONE = 8;  // barriers in turn for finished S and for finished O
+  static constexpr int SMEM_BYTES = OFF_BAR + 512;
+  static constexpr uint32_t TMEM_COLS = 256;
+  static constexpr uint32_t TM_S = 0, TM_O = 128;
+  static_assert(PER_SM * (SMEM_BYTES + 1024) <= 233472, "CTAs per SM");
+  static_assert(DONE > UNITS / 2 + 1, "a slot's barrier is read before it comes round again");
+  static_assert(8 * (UNITS + 2 * DONE + 4) + 8 + 8 * 4 <= 512, "barrier area");
+};
+
+// 2^x for a pair on the FMA pipe, as exp2_fma2, with a NaN kept (the clamp and the last step let it through).
+__device__ __forceinline__ float2 exp2_fma2_nan(float2 x) {
+  x.x = max_nan(x.x, -125.0f);
+  x.y = max_nan(x.y, -125.0f);
+  const float2 t = fadd2(x, make_float2(12582912.0f, 12582912.0f));
+  const float2 j = fadd2(t, make_float2(-12582912.0f, -12582912.0f));
+  const float2 f = fadd2(x, make_float2(-j.x, -j.y));
+  float2 p = ffma2(make_float2(0.0551716685f, 0.0551716685f), f, make_float2(0.242611125f, 0.242611125f));
+  p = ffma2(p, f, make_float2(0.693260968f, 0.693260968f));
+  p = ffma2(p, f, make_float2(0.999928057f, 0.999928057f));
+  const float2 two_j = make_float2(__int_as_float((__float_as_int(t.x) << 23) + 0x3f800000),
+                                   __int_as_float((__float_as_int(t.y) << 23) + 0x3f800000));
+  return ffma2(p, two_j, make_float2(0.f, 0.f));
+}
+
+// Every PACKED_POLY-th pair of exponentials goes to the FMA pipe.
+#ifndef PACKED_POLY
+#define PACKED_POLY 8
+#endif
+
+// P for 64 keys of one row: 2^(s c - mc), rounded, into 32 columns of tensor memory; with SUM returns the
+// sum of the unrounded values.  Masked scores are -infinity.
 template <typename T, bool MASK, bool SUM>
-__device__ __forceinline__ float packed_sub_p(const float (&s)[64], float c, float mc, int valid, uint32_t t_p,
-                                              uint64_t* full) {
+__device__ __forceinline__ float packed_p64(const float (&s)[64], float c, float mc, int valid, uint32_t t_p) {
   const float2 cc = make_float2(c, c);
   const float2 nm = make_float2(-mc, -mc);
   float2 l0 = make_float2(0.f, 0.f), l1 = l0;
@@ -179,12 +226,12 @@ __device__ __forceinline__ float packed_sub_p(const float (&s)[64], float c, flo
   for (int b = 0; b < 2; ++b) {
     uint32_t pk[16];
 #pragma unroll
-    for (int u = 0; u < 32; u += 2) {
-      const int t = b * 32 + u;
+    for (int u = 0; u < 16; ++u) {
+      const int t = b * 32 + u * 2;
       const float2 x = ffma2(make_float2(s[t], s[t + 1]), cc, nm);
       float2 e;
-      if ((t & (kPolyEvery - 1)) == kPolyEvery - 2) {
-        e = exp2_fma2(x);
+      if ((t >> 1) % PACKED_POLY == PACKED_POLY - 1) {
+        e = exp2_fma2_nan(x);
         if (MASK) {
           e.x = (t < valid) ? e.x : 0.f;
           e.y = (t + 1 < valid) ? e.y : 0.f;
@@ -193,28 +240,25 @@ __device__ __forceinline__ float packed_sub_p(const float (&s)[64], float c, flo
         e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
       }
       if (SUM) {
-        if (u & 2)
+        if (u & 1)
           l1 = fadd2(l1, e);
         else
           l0 = fadd2(l0, e);
       }
-      pk[u >> 1] = pack2<T>(e.x, e.y);
+      pk[u] = pack2<T>(e.x, e.y);
     }
     tmem_st16_nowait(t_p + b * 16, pk);
   }
-  tmem_st_wait();
-  tc_fence_before();
-  mbar_arrive(full);
   return (l0.x + l0.y) + (l1.x + l1.y);
 }
 
 template <typename T, int HD>
-__global__ void __launch_bounds__(ATT_THREADS, 2)
+__global__ void __launch_bounds__(ATT_THREADS, AttnPackedCfg<HD>::PER_SM)
     attn_packed_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV, const __grid_constant__ AttnPackedParams p,
                        int* status) {
   using Cfg = AttnPackedCfg<HD>;
-  constexpr int UNITS = Cfg::UNITS;
+  constexpr int UNITS = Cfg::UNITS, DONE = Cfg::DONE;
   int* gstatus = op_status(status);
   const unsigned long long wlim = p.wait_ns;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -225,11 +269,10 @@ __global__ void __launch_bounds__(ATT_THREADS, 2)
   }
   uint8_t* ring = smem + Cfg::OFF_RING;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + Cfg::OFF_BAR);  // [UNITS]
-  uint64_t* empty = full + UNITS;                                     // [UNITS]
-  uint64_t* s_full = empty + UNITS;                                   // [2]
-  uint64_t* p_full = s_full + 2;                                      // [2]
-  uint64_t* pv_done = p_full + 2;
-  uint64_t* mma_done = pv_done + 1;
+  uint64_t* s_done = full + UNITS;                                    // [DONE] S of block n
+  uint64_t* pv_done = s_done + DONE;                                  // [DONE] O of block n
+  uint64_t* p_full = pv_done + DONE;                                  // [2] P in an S buffer
+  uint64_t* mma_done = p_full + 2;
   uint64_t* q_full = mma_done + 1;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(q_full + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
@@ -237,20 +280,18 @@ __global__ void __launch_bounds__(ATT_THREADS, 2)
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int h = blockIdx.y;
-  const int hk = h / (p.Hq / p.Hkv);
+  const int h0 = blockIdx.y * p.pack;  // first query head
+  const int hk = h0 / (p.Hq / p.Hkv);
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
-    for (int s = 0; s < UNITS; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+    for (int s = 0; s < UNITS; ++s) mbar_init(&full[s], 1);
+    for (int s = 0; s < DONE; ++s) {
+      mbar_init(&s_done[s], 1);
+      mbar_init(&pv_done[s], 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 128);
-    }
-    mbar_init(pv_done, 1);
+    mbar_init(&p_full[0], 128);
+    mbar_init(&p_full[1], 128);
     mbar_init(mma_done, 1);
     fence_mbar_init();
     tma_prefetch_desc(&tmQ);
@@ -273,7 +314,7 @@ __global__ void __launch_bounds__(ATT_THREADS, 2)
   pdl_wait();
   if (threadIdx.x == 0) *abort_flag = (*reinterpret_cast<volatile int*>(gstatus) != 0) ? 1 : 0;
   if (warp == 2) {
-    const SeqTile f = find_tile(p, static_cast<int>(blockIdx.x), ATT_BM, 1);
+    const SeqTile f = find_tile(p, static_cast<int>(blockIdx.x), p.tokens);
     if (lane == 0) *s_tile = f;
   }
   pdl_launch_dependents();
@@ -284,96 +325,99 @@ __global__ void __launch_bounds__(ATT_THREADS, 2)
   SeqTile st = *s_tile;
   const bool skip = *abort_flag != 0 || st.seq < 0;
   // the longest tiles first: with a causal mask the last tile of a sequence sees the most keys
-  if (p.causal && !skip) st.tile = (st.lq + ATT_BM - 1) / ATT_BM - 1 - st.tile;
-  const int row0 = st.tile * ATT_BM;
-  const int off = st.lk - st.lq;  // causal: row t sees keys 0 .. t + off
-  const int kend = p.causal ? clampi(min(row0 + ATT_BM, st.lq) + off, 0, st.lk) : st.lk;
-  const int nsub = skip ? 0 : (kend + 63) / 64;
-  // ring position of the K and V tiles of sub-block n: K0 | K1 V0 | K2 V1 | ... | V(nsub-1)
+  if (p.causal && !skip) st.tile = (st.lq + p.tokens - 1) / p.tokens - 1 - st.tile;
+  const int tok0 = st.tile * p.tokens;
+  const int off = st.lk - st.lq;  // causal: query t sees keys 0 .. t + off
+  const int kend = p.causal ? clampi(min(tok0 + p.tokens, st.lq) + off, 0, st.lk) : st.lk;
+  const int nblk = skip ? 0 : (kend + 63) / 64;
+  // place in the ring of the K and V tiles of block n: K0 | K1 V0 | K2 V1 | ... | V(nblk-1)
   auto pos_k = [](int n) { return n == 0 ? 0 : 2 * n - 1; };
-  auto pos_v = [nsub](int n) { return n + 1 < nsub ? 2 * n + 2 : 2 * n + 1; };
+  auto pos_v = [nblk](int n) { return n + 1 < nblk ? 2 * n + 2 : 2 * n + 1; };
 
-  if (nsub > 0 && warp == 0 && lane == 0) {
+  if (nblk > 0 && warp == 0 && lane == 0) {
     // ------------------------------------------------------------------ TMA producer
     int issued_parity[UNITS];
 #pragma unroll
     for (int s = 0; s < UNITS; ++s) issued_parity[s] = -1;
-    mbar_arrive_expect_tx(q_full, Cfg::Q_BYTES);
+    const int q_bytes = p.tokens * p.pack * 128;  // of a slab of 64 values
+    mbar_arrive_expect_tx(q_full, q_bytes * (HD / 64));
 #pragma unroll
     for (int c = 0; c < HD / 64; ++c)
-      tma_load_3d(smem + Cfg::OFF_Q + c * 16384, &tmQ, c * 64, h, st.q0 + row0, q_full);
-    int slot = 0;
-    uint32_t ph = 0;
-    auto load = [&](const CUtensorMap* tm, int key) {
-      if (!mbar_wait(&empty[slot], ph ^ 1u, abort_flag, gstatus, DEV_TIMEOUT_ATTP + 1, wlim)) return false;
+      tma_load_3d(smem + Cfg::OFF_Q + c * 16384, &tmQ, c * 64, h0, st.q0 + tok0, q_full);
+    for (int pos = 0; pos < 2 * nblk; ++pos) {
+      const int slot = pos % UNITS;
+      if (pos >= UNITS) {  // the slot's last tile has been used: K by its S, V by its O
+        const int old = pos - UNITS;
+        const bool was_k = old == 0 || (old & 1);
+        const int b = was_k ? (old + 1) >> 1 : (old >> 1) - 1;
+        if (!mbar_wait(&(was_k ? s_done : pv_done)[b % DONE], static_cast<uint32_t>(b / DONE) & 1u, abort_flag, gstatus,
+                       DEV_TIMEOUT_ATTP + 1, wlim))
+          break;
+      }
+      const bool is_k = pos == 0 || ((pos & 1) && pos != 2 * nblk - 1);
+      const int b = is_k ? (pos + 1) >> 1 : (pos == 2 * nblk - 1 ? nblk - 1 : (pos >> 1) - 1);
       mbar_arrive_expect_tx(&full[slot], Cfg::UNIT);
 #pragma unroll
-      for (int c = 0; c < HD / 64; ++c) tma_load_3d(ring + slot * Cfg::UNIT + c * 8192, tm, c * 64, hk, key, &full[slot]);
-      issued_parity[slot] = static_cast<int>(ph);
-      if (++slot == UNITS) {
-        slot = 0;
-        ph ^= 1u;
-      }
-      return true;
-    };
-    bool ok = true;
-    for (int n = 0; ok && n <= nsub; ++n) {
-      if (n < nsub) ok = load(&tmK, st.k0 + n * 64);
-      if (ok && n > 0) ok = load(&tmV, st.k0 + (n - 1) * 64);
+      for (int c = 0; c < HD / 64; ++c)
+        tma_load_3d(ring + slot * Cfg::UNIT + c * 8192, is_k ? &tmK : &tmV, c * 64, hk, st.k0 + b * 64, &full[slot]);
+      issued_parity[slot] = (pos / UNITS) & 1;
     }
     if (*abort_flag) {
       mbar_wait_drain(q_full, 0);
       for (int s = 0; s < UNITS; ++s)
         if (issued_parity[s] >= 0) mbar_wait_drain(&full[s], static_cast<uint32_t>(issued_parity[s]));
     }
-  } else if (nsub > 0 && warp == 1) {
+  } else if (nblk > 0 && warp == 1) {
     // ------------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
+    if (elect_one()) {
       constexpr uint32_t idesc_s = idesc_of<T>(ATT_BM, 64, false);
       constexpr uint32_t idesc_o = idesc_of<T>(ATT_BM, Cfg::O_COLS, true);
-      const uint32_t q0 = smem_u32(smem + Cfg::OFF_Q);
-      const uint32_t r0 = smem_u32(ring);
-      const uint32_t ones0 = smem_u32(smem + Cfg::OFF_ONES);
-      const uint32_t t_s0 = tmem_base + Cfg::TM_S, t_o0 = tmem_base + Cfg::TM_O;
+      const uint64_t dq = sdesc_sw128(smem_u32(smem + Cfg::OFF_Q), 16, 1024);
+      const uint32_t r0 = smem_u32(ring), ones0 = smem_u32(smem + Cfg::OFF_ONES);
+      const uint64_t dk0 = sdesc_sw128(r0, 16, 1024);
+      const uint32_t full0 = smem_u32(full), p_full0 = smem_u32(p_full);
+      const uint32_t t_s = tmem_base + Cfg::TM_S, t_o = tmem_base + Cfg::TM_O;
+      uint32_t kslot = 0, kph = 0;  // of the next K
+      auto have_k = [&]() { return wait_one(full0 + kslot * 8, kph, abort_flag, gstatus, DEV_TIMEOUT_ATTP + 3, wlim); };
       auto issue_s = [&](int n) {
-        const uint32_t kb = r0 + (pos_k(n) % UNITS) * Cfg::UNIT;
-        const uint64_t dq = sdesc_sw128(q0, 16, 1024), dk = sdesc_sw128(kb, 16, 1024);
+        const uint64_t dk = dk0 + kslot * (Cfg::UNIT >> 4);
+        const uint32_t d = t_s + 64 * (n & 1);
 #pragma unroll
-        for (int k = 0; k < HD / 16; ++k)  // 16 values of the width each; 64 per 128-byte atom
-          tc_mma_ss(t_s0 + 64 * (n & 1), dq + (k >> 2) * (16384 >> 4) + (k & 3) * 2,
-                    dk + (k >> 2) * (8192 >> 4) + (k & 3) * 2, idesc_s, k != 0 ? 1u : 0u);
-        tc_commit(&s_full[n & 1]);
-        tc_commit(&empty[pos_k(n) % UNITS]);
-      };
-      auto wait_unit = [&](int pos, int site) {
-        const bool got = mbar_wait<32>(&full[pos % UNITS], static_cast<uint32_t>(pos / UNITS) & 1u, abort_flag, gstatus,
-                                       DEV_TIMEOUT_ATTP + site, wlim);
-        tc_fence_after();
-        return got;
-      };
-      bool ok = mbar_wait<32>(q_full, 0, abort_flag, gstatus, DEV_TIMEOUT_ATTP + 2, wlim) && wait_unit(pos_k(0), 3);
-      if (ok) issue_s(0);
-      if (ok && nsub > 1) {
-        ok = wait_unit(pos_k(1), 3);
-        if (ok) issue_s(1);
-      }
-      for (int n = 0; ok && n < nsub; ++n) {
-        ok = mbar_wait<32>(&p_full[n & 1], static_cast<uint32_t>(n >> 1) & 1u, abort_flag, gstatus,
-                           DEV_TIMEOUT_ATTP + 4, wlim) &&
-             wait_unit(pos_v(n), 5);
-        if (!ok) break;
-        const uint32_t vb = r0 + (pos_v(n) % UNITS) * Cfg::UNIT;
-        const uint64_t dv = sdesc_sw128(vb, Cfg::ONES ? ones0 - vb : 8192u, 1024);
-        const uint32_t tp = t_s0 + 64 * (n & 1);
-        const uint32_t a_p[4] = {tp, tp + 8, tp + 16, tp + 24};
-        const uint64_t b_v[4] = {dv, dv + 128, dv + 256, dv + 384};
-        tc_mma_ts_chain4(t_o0, a_p, b_v, idesc_o, n > 0 ? 1u : 0u);
-        tc_commit(pv_done);
-        tc_commit(&empty[pos_v(n) % UNITS]);
-        if (n + 2 < nsub) {
-          ok = wait_unit(pos_k(n + 2), 6);
-          if (ok) issue_s(n + 2);
+        for (int k = 0; k < HD / 16; ++k)  // 16 values of the width each; 64 a slab
+          tc_mma_ss(d, dq + (k >> 2) * (16384 >> 4) + (k & 3) * 2, dk + (k >> 2) * (8192 >> 4) + (k & 3) * 2, idesc_s,
+                    k != 0 ? 1u : 0u);
+        tc_commit(&s_done[n % DONE]);
+        kslot += n == 0 ? 1 : 2;  // K0 | K1 V0 | K2 V1 ...
+        if (kslot >= UNITS) {
+          kslot -= UNITS;
+          kph ^= 1u;
         }
+      };
+      bool ok = wait_one(smem_u32(q_full), 0, abort_flag, gstatus, DEV_TIMEOUT_ATTP + 2, wlim);
+#pragma unroll 1
+      for (int n = 0; ok && n < 2 && n < nblk; ++n) {
+        ok = have_k();
+        tc_fence_after();
+        if (ok) issue_s(n);
+      }
+#pragma unroll 1
+      for (int n = 0; ok && n < nblk; ++n) {
+        const int pos = pos_v(n);
+        const uint32_t slot = static_cast<uint32_t>(pos % UNITS);
+        const uint32_t vb = r0 + slot * Cfg::UNIT;
+        const uint64_t dv = sdesc_sw128(vb, Cfg::ONES ? ones0 - vb : 8192u, 1024);
+        const uint32_t tp = t_s + 64 * (n & 1);
+        ok = wait_one(full0 + slot * 8, static_cast<uint32_t>(pos / UNITS) & 1u, abort_flag, gstatus, DEV_TIMEOUT_ATTP + 5,
+                      wlim) &&
+             (n + 2 >= nblk || have_k()) &&
+             wait_one(p_full0 + (n & 1) * 8, static_cast<uint32_t>(n >> 1) & 1u, abort_flag, gstatus, DEV_TIMEOUT_ATTP + 4,
+                      wlim);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) tc_mma_ts(t_o, tp + 8 * k, dv + 128 * k, idesc_o, n > 0 || k > 0 ? 1u : 0u);
+        tc_commit(&pv_done[n % DONE]);
+        if (n + 2 < nblk) issue_s(n + 2);  // into the buffer that P has just left: MMAs run in order
       }
       tc_commit(mma_done);
     }
@@ -382,41 +426,45 @@ __global__ void __launch_bounds__(ATT_THREADS, 2)
     // ------------------------------------------------------------------ softmax
     const int q = warp & 3;
     const int r = q * 32 + lane;
-    const int row = row0 + r;
+    const int tt = r / p.pack;
+    const int tok = tok0 + tt;
+    const bool mine = tt < p.tokens && tok < st.lq;
     const uint32_t lane_off = static_cast<uint32_t>(q * 32) << 16;
     const uint32_t t_s = tmem_base + lane_off + Cfg::TM_S;
     const uint32_t t_o = tmem_base + lane_off + Cfg::TM_O;
-    const int lim = p.causal ? min(st.lk, row + off + 1) : st.lk;  // keys this row sees (<= 0: none)
+    // keys this row sees (<= 0: none); rows of nobody go along with the last one
+    const int lim = p.causal ? min(st.lk, min(tok, st.lq - 1) + off + 1) : st.lk;
     const float c = p.scale_log2;
     float m = -INFINITY, l = 0.f;
     bool ok = true;
-    for (int n = 0; n < nsub; ++n) {
-      const int buf = n & 1;
-      if (!mbar_wait_warp(&s_full[buf], static_cast<uint32_t>(n >> 1) & 1u, abort_flag, gstatus, DEV_TIMEOUT_ATTP + 7,
-                          wlim)) {
+    for (int n = 0; n < nblk; ++n) {
+      if (!wait_warp(smem_u32(s_done) + (n % DONE) * 8, static_cast<uint32_t>(n / DONE) & 1u, abort_flag, gstatus, DEV_TIMEOUT_ATTP + 7,
+                     wlim)) {
         ok = false;
         break;
       }
       tc_fence_after();
+      const uint32_t t_b = t_s + 64 * (n & 1);
       float s[64];
       __syncwarp();
-      tmem_ld64(t_s + 64 * buf, s);
+      tmem_ld64(t_b, s);
       const int valid = lim - n * 64;
       const bool part = __any_sync(0xffffffffu, valid < 64);
       if (part) {
 #pragma unroll
         for (int t = 0; t < 64; ++t) s[t] = (t < valid) ? s[t] : -INFINITY;
       }
-      const float m_new = maxn(m, row_maxn64(s));
-      const bool resc = !((m_new - m) * c <= kRescaleLog2) && m_new != -INFINITY;  // a NaN moves it too
+      const float m_new = fmaxf(m, row_max64(s));
+      const bool resc = !((m_new - m) * c <= kRescaleLog2) && m_new != -INFINITY;
       float alpha = 1.f;
       if (resc) {
-        alpha = ex2_approx((m - m_new) * c);
+        alpha = to_max(m, m_new, c);
         m = m_new;
+        l *= alpha;
       }
       if (n > 0 && __any_sync(0xffffffffu, resc)) {
-        if (!mbar_wait_warp(pv_done, static_cast<uint32_t>(n - 1) & 1u, abort_flag, gstatus, DEV_TIMEOUT_ATTP + 8,
-                            wlim)) {
+        if (!wait_warp(smem_u32(pv_done) + ((n - 1) % DONE) * 8, static_cast<uint32_t>((n - 1) / DONE) & 1u, abort_flag, gstatus,
+                       DEV_TIMEOUT_ATTP + 8, wlim)) {
           ok = false;
           break;
         }
@@ -431,17 +479,16 @@ __global__ void __launch_bounds__(ATT_THREADS, 2)
           tmem_st16(t_o + u, ob);
         }
       }
-      if (n == nsub - 1 && st.lk < nsub * 64) {
+      if (n == nblk - 1 && st.lk < nblk * 64) {
         // V rows past the sequence's keys: zeros
         const int pos = pos_v(n);
-        if (!mbar_wait_warp(&full[pos % UNITS], static_cast<uint32_t>(pos / UNITS) & 1u, abort_flag, gstatus,
-                            DEV_TIMEOUT_ATTP + 9, wlim)) {
+        if (!wait_warp(smem_u32(&full[pos % UNITS]), static_cast<uint32_t>(pos / UNITS) & 1u, abort_flag, gstatus,
+                       DEV_TIMEOUT_ATTP + 9, wlim)) {
           ok = false;
           break;
         }
-        const int from = st.lk - n * 64;
         uint4* vt = reinterpret_cast<uint4*>(ring + (pos % UNITS) * Cfg::UNIT);
-        for (int i = from * 8 + r; i < 512; i += 128) {
+        for (int i = (st.lk - n * 64) * 8 + r; i < 512; i += 128) {
 #pragma unroll
           for (int a = 0; a < HD / 64; ++a) vt[a * 512 + i] = make_uint4(0u, 0u, 0u, 0u);
         }
@@ -449,35 +496,38 @@ __global__ void __launch_bounds__(ATT_THREADS, 2)
       }
       const float mc = max_offset(m, c);
       __syncwarp();
-      l = l * alpha + (part ? packed_sub_p<T, true, !Cfg::ONES>(s, c, mc, valid, t_s + 64 * buf, &p_full[buf])
-                            : packed_sub_p<T, false, !Cfg::ONES>(s, c, mc, valid, t_s + 64 * buf, &p_full[buf]));
+      l += part ? packed_p64<T, true, !Cfg::ONES>(s, c, mc, valid, t_b) : packed_p64<T, false, !Cfg::ONES>(s, c, mc, valid, t_b);
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(&p_full[n & 1]);
     }
-    if (ok && nsub > 0) ok = mbar_wait_warp(mma_done, 0, abort_flag, gstatus, DEV_TIMEOUT_ATTP + 10, wlim);
+    if (ok && nblk > 0) ok = wait_warp(smem_u32(mma_done), 0, abort_flag, gstatus, DEV_TIMEOUT_ATTP + 10, wlim);
     if (ok) {
       tc_fence_after();
-      if (Cfg::ONES && nsub > 0) {
+      const bool sees = lim > 0 && nblk > 0;
+      if (Cfg::ONES && nblk > 0) {
         float ls[16];
         __syncwarp();
         tmem_ld16(t_o + 64, ls);
         l = ls[0];
       }
-      const float inv = (lim > 0 && nsub > 0) ? 1.0f / l : 0.f;
-      T* dst = static_cast<T*>(p.out) + static_cast<int64_t>(st.q0 + row) * p.o_tok + h * p.o_head;
+      const float inv = sees ? 1.0f / l : 0.f;
+      T* dst = static_cast<T*>(p.out) + static_cast<int64_t>(st.q0 + tok) * p.o_tok +
+               static_cast<int64_t>(h0 + r - tt * p.pack) * p.o_head;
 #pragma unroll 1
       for (int u = 0; u < HD; u += 64) {
         float o[64];
         __syncwarp();
-        if (nsub > 0) tmem_ld64(t_o + u, o);
-        if (row < st.lq) {
+        if (nblk > 0) tmem_ld64(t_o + u, o);
+        if (mine) {
           uint4* d4 = reinterpret_cast<uint4*>(dst + u);
 #pragma unroll
           for (int t = 0; t < 8; ++t)
-            d4[t] = lim > 0 && nsub > 0
-                        ? make_uint4(pack2<T>(o[8 * t + 0] * inv, o[8 * t + 1] * inv),
-                                     pack2<T>(o[8 * t + 2] * inv, o[8 * t + 3] * inv),
-                                     pack2<T>(o[8 * t + 4] * inv, o[8 * t + 5] * inv),
-                                     pack2<T>(o[8 * t + 6] * inv, o[8 * t + 7] * inv))
-                        : make_uint4(0u, 0u, 0u, 0u);
+            d4[t] = sees ? make_uint4(pack2<T>(o[8 * t + 0] * inv, o[8 * t + 1] * inv),
+                                      pack2<T>(o[8 * t + 2] * inv, o[8 * t + 3] * inv),
+                                      pack2<T>(o[8 * t + 4] * inv, o[8 * t + 5] * inv),
+                                      pack2<T>(o[8 * t + 6] * inv, o[8 * t + 7] * inv))
+                         : make_uint4(0u, 0u, 0u, 0u);
         }
       }
     }
@@ -486,7 +536,7 @@ __global__ void __launch_bounds__(ATT_THREADS, 2)
   // ------------------------------------------------------------------ teardown
   __syncthreads();
   if (warp == 1) {
-    if (nsub > 0 && lane == 0) mbar_wait_drain(mma_done, 0);
+    if (nblk > 0 && lane == 0) mbar_wait_drain(mma_done, 0);
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem_base, Cfg::TMEM_COLS);

@@ -164,9 +164,6 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
   const T* h = reinterpret_cast<const T*>(&hi);
   lo = pack2<T>(x - to_f32<T>(h[0]), y - to_f32<T>(h[1]));
 }
-// Factor that brings sums at maximum m to the common maximum top.
-__device__ __forceinline__ float to_max(float m, float top, float c) { return m == top ? 1.f : ex2_approx((m - top) * c); }
-
 template <typename T, int HD>
 __global__ void __launch_bounds__(ATTR_THREADS, AttnRowsCfg<HD>::PER_SM)
     attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,

@@ -127,10 +127,10 @@ bool tmap_out16(CUtensorMap* tm, void* base, int64_t cols, int64_t rows, int64_t
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// 3-D map of heads [tokens, heads, d] of a 16-bit type: box 64 values x 1 head x box_tokens.  The
+// 3-D map of heads [tokens, heads, d] of a 16-bit type: box 64 values x box_heads x box_tokens.  The
 // values only move, so the type of the map does not matter.
 bool tmap_heads(CUtensorMap* tm, const void* base, int d, int heads, int64_t tokens, int64_t head_ld, int64_t tok_ld,
-                uint32_t box_tokens) {
+                uint32_t box_tokens, uint32_t box_heads = 1) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(tokens)};
@@ -138,7 +138,7 @@ bool tmap_heads(CUtensorMap* tm, const void* base, int d, int heads, int64_t tok
   if (heads == 1) head_ld = d;
   if (tokens == 1) tok_ld = d;
   cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_ld) * 2, static_cast<cuuint64_t>(tok_ld) * 2};
-  cuuint32_t box[3] = {64, 1, box_tokens};
+  cuuint32_t box[3] = {64, box_heads, box_tokens};
   cuuint32_t estr[3] = {1, 1, 1};
   return fn(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -231,8 +231,8 @@ cudaError_t launch_attn_packed(const CUtensorMap& q, const CUtensorMap& k, const
   cudaError_t e = set_smem_attr_once(attn_packed_kernel<T, HD>, smem, attr_done);
   if (e != cudaSuccess) return e;
   // n sequences of Tq rows in all need at most this many tiles
-  const long long tiles = static_cast<long long>(p.Tq) / ATT_BM + p.n;
-  return launch_pdl(attn_packed_kernel<T, HD>, dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(p.Hq)),
+  const long long tiles = static_cast<long long>(p.Tq) / p.tokens + p.n;
+  return launch_pdl(attn_packed_kernel<T, HD>, dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(p.Hq / p.pack)),
                     dim3(ATT_THREADS), smem, s, q, k, v, p, st);
 }
 
@@ -488,7 +488,7 @@ vit_status vit_op_attention_packed(const vit_attn_packed* a, vit_stream_t stream
   const int64_t strides[8] = {a->q_token, a->q_head, a->k_token, a->k_head, a->v_token, a->v_head, a->out_token, a->out_head};
   for (int64_t s : strides)
     if (s % 8 || s < 0 || s >= (1LL << 38)) return fail(VIT_E_SHAPE, "strides must be multiples of 8, not negative");
-  if (static_cast<int64_t>(a->n) + a->Tq / ATT_BM > 0x7fffffffLL) return fail(VIT_E_SHAPE, "too many sequences");
+  if (static_cast<int64_t>(a->n) + a->Tq > 0x7fffffffLL) return fail(VIT_E_SHAPE, "too many sequences");
   const bool rows = takes_rows_kernel(a);
   if (rows && (!a->workspace || !aligned16(a->workspace) || a->workspace_bytes < rows_workspace(a->head_dim)))
     return fail(VIT_E_WORKSPACE, "workspace missing, not 16-byte aligned or too small");
@@ -516,12 +516,18 @@ vit_status vit_op_attention_packed(const vit_attn_packed* a, vit_stream_t stream
   p.causal = a->causal != 0;
   p.scale_log2 = a->scale * 1.4426950408889634f;
   p.wait_ns = a->wait_ns;
+  // As many of the heads that share a key head in a tile as divide their number and fill 120 of 128 rows
+  const int group = a->heads_q / a->heads_k;
+  p.pack = 1;
+  for (int x = 2; x <= std::min(group, 128); ++x)
+    if (group % x == 0 && 128 / x * x >= 120) p.pack = x;
+  p.tokens = 128 / p.pack;
   CUtensorMap tq, tk, tv;
   // without keys nothing is loaded: any valid map will do
   const void* kb = a->Tk > 0 ? a->k : a->q;
   const void* vb = a->Tk > 0 ? a->v : a->q;
   const int64_t tkeys = std::max<int64_t>(1, a->Tk);
-  if ((!rows && !tmap_heads(&tq, a->q, a->head_dim, a->heads_q, a->Tq, a->q_head, a->q_token, ATT_BM)) ||
+  if ((!rows && !tmap_heads(&tq, a->q, a->head_dim, a->heads_q, a->Tq, a->q_head, a->q_token, p.tokens, p.pack)) ||
       !tmap_heads(&tk, kb, a->head_dim, a->heads_k, tkeys, a->k_head, a->k_token, 64) ||
       !tmap_heads(&tv, vb, a->head_dim, a->heads_k, tkeys, a->v_head, a->v_token, 64))
     return no_map();
