@@ -731,3 +731,28 @@ def test_linear_split_and_tile_wait_expiry_is_reported(M, N, K):
     V.linear_fp8(a, sa, w, sw, bias=b, out=out)
     V.op_poll()
     check_linear(out, a, sa, w, sw, b)
+
+
+@pytest.mark.parametrize("rows,D", [(6000, 64), (9000, 256), (7001, 512), (5003, 1024), (6001, 2048), (3001, 4096), (2001, 8200),
+                                    (1500, 16384), (5000, 1023)])
+@pytest.mark.parametrize("xt", ["bf16", "fp16"])
+def test_many_rows(rows, D, xt):
+    """As many rows as run through the ring of copies: every row is right, quantised and normed."""
+    V, g = lib(), gen(rows)
+    x = randn(g, rows, D, dtype=DT[xt], scale=4.0)
+    x[rows // 2] = 0
+    q, s = V.quant_rows(x)
+    check_rows8(q, s, x.double(), (rows, D))
+    w = (1 + randn(g, D, scale=0.3)).to(DT[xt])
+    for weight in (w, w.float()):
+        for e4m3 in (True, False):
+            out, scales, _ = V.rms_norm(x, weight, 1e-6, fp8=e4m3)
+            y = x.double() / torch.sqrt(x.double().square().mean(dim=1, keepdim=True) + 1e-6) * w.double()
+            if e4m3:
+                check_rows8(out, scales, y, (rows, D))
+            else:
+                tiny = 2.0 ** -25 if xt == "fp16" else 0.0
+                assert ((out.double() - y).abs() <= y.abs() * (u_of(x.dtype) + NORM32) * 1.01 + tiny).all()
+    few, _, _ = V.rms_norm(x[:3], w, 1e-6)
+    many, _, _ = V.rms_norm(x, w, 1e-6)
+    assert ((few.double() - many[:3].double()).abs() <= 2 * u_of(x.dtype) * many[:3].double().abs()).all()

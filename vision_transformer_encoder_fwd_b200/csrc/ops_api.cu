@@ -1,6 +1,7 @@
 // Host side of the operator entry points in include/vit_ops.h: checks, tensor maps, launches.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "../../include/vit_ops.h"
 #include "attention_packed.cuh"
@@ -46,9 +47,43 @@ cudaError_t launch_rows(const RowsParams& p, bool vec, cudaStream_t s) {
     const int t = whole_warps((p.D + per_thread - 1) / per_thread);
     return t > 32 && t < 128 ? 128 : t;
   };
+  // Many rows without a residual go through the ring kernel: from one row a block on it has nothing to gain.  A
+  // thread takes 32 values where there are as many, since a row costs it about 100 instructions whatever
+  // its share (16 values: 25 us where 32 take 23).
+  if constexpr (RMODE == 0 && sizeof(TX) == 2) {
+    auto ring = [&](auto nv, int tpr, bool& taken) {
+      constexpr int NV = decltype(nv)::value, STAGES = 4;
+      const int block = tpr == 32 ? 128 : tpr;  // several rows share a block only where a warp has one
+      const int block_rows = block / tpr;
+      const int smem = STAGES * NV * block * 16;
+      const int64_t at_once = static_cast<int64_t>(std::min(768 / block, 226 * 1024 / (smem + 2048))) * current_sms();
+      taken = (p.rows + block_rows - 1) / block_rows > at_once;
+      if (!taken) return cudaSuccess;
+      static std::atomic<uint64_t> done{0};
+      auto kernel = rows_stream_kernel<TX, OUT8, NV, STAGES>;
+      cudaError_t e = set_smem_attr_once(kernel, 128 * 1024, done);
+      if (e != cudaSuccess) return e;
+      return launch_pdl(kernel, dim3(static_cast<unsigned>(at_once)), dim3(block), smem, s, p, tpr);
+    };
+    if (vec && p.D <= 16384) {
+      bool taken = false;
+      cudaError_t e;
+      if (p.D <= 256)
+        e = ring(std::integral_constant<int, 1>{}, 32, taken);
+      else if (p.D <= 512)
+        e = ring(std::integral_constant<int, 2>{}, 32, taken);
+      else
+        e = ring(std::integral_constant<int, 4>{},
+                 p.D <= 1024 ? 32 : p.D <= 2048 ? 64 : std::max(128, whole_warps((p.D + 31) / 32)), taken);
+      if (taken) return e;
+    }
+  }
   if (vec) {
+    // 8 values a thread where that fills 128 threads (16384 rows of 1024: 24-26 us, 28-29 with 16)
     if (p.D <= 256) return go(rows_kernel<TX, RMODE, OUT8, 8, 1>, 32);
-    if (p.D <= 16384) return go(rows_kernel<TX, RMODE, OUT8, 8, 2>, tpr_of(16));
+    if (p.D <= 512) return go(rows_kernel<TX, RMODE, OUT8, 8, 2>, 32);
+    if (p.D <= 2048) return go(rows_kernel<TX, RMODE, OUT8, 8, 1>, tpr_of(8));
+    if (p.D <= 8192) return go(rows_kernel<TX, RMODE, OUT8, 8, 2>, tpr_of(16));
     return go(rows_kernel<TX, RMODE, OUT8, 8, 4>, tpr_of(32));
   }
   if (p.D <= 8192) return go(rows_kernel<TX, RMODE, OUT8, 1, 8>, tpr_of(8));
@@ -404,8 +439,14 @@ vit_status vit_op_rope(const vit_rope_tensor* q, const vit_rope_tensor* k, vit_d
   if (!std::isfinite(gain)) return fail(VIT_E_INVALID_ARG, "gain must be finite");
   const vit_rope_tensor* tq[2] = {q, k};
   const int n = rotary_dim / 2;
-  const int e = type == VIT_DT_F32 ? 4 : 8;
-  bool vec = (layout == VIT_ROPE_HALF ? n : rotary_dim) % e == 0 && (head_dim - rotary_dim) % e == 0;
+  const int size = static_cast<int>(type_size(type));
+  // bytes an access: what every chunk's place and every row's stride is a multiple of
+  int64_t even = 16 / size;
+  auto share = [&even](int64_t v) {
+    while (v % even) even /= 2;
+  };
+  share(layout == VIT_ROPE_HALF ? n : rotary_dim);
+  share(head_dim - rotary_dim);
   RopeParams p{};
   for (int i = 0; i < 2; ++i) {
     if (!tq[i] || !tq[i]->in || tq[i]->heads == 0) continue;
@@ -420,8 +461,8 @@ vit_status vit_op_rope(const vit_rope_tensor* q, const vit_rope_tensor* k, vit_d
     p.out_tok[i] = t.out_token;
     p.out_head[i] = t.out_head;
     p.heads[i] = t.heads;
-    vec = vec && aligned16(t.in) && aligned16(t.out) && t.in_token % e == 0 && t.in_head % e == 0 &&
-          t.out_token % e == 0 && t.out_head % e == 0;
+    for (int64_t v : {t.in_token, t.in_head, t.out_token, t.out_head}) share(v);
+    for (const void* v : {t.in, static_cast<const void*>(t.out)}) share(static_cast<int64_t>(reinterpret_cast<uintptr_t>(v) / size));
   }
   if (T == 0 || p.heads[0] + p.heads[1] == 0) return VIT_OK;
   if (!positions || !aligned_to(positions, pos64 ? 8 : 4)) return fail(VIT_E_INVALID_ARG, "positions NULL or misaligned");
@@ -453,16 +494,20 @@ vit_status vit_op_rope(const vit_rope_tensor* q, const vit_rope_tensor* k, vit_d
                       reinterpret_cast<cudaStream_t>(stream), p);
   };
   cudaError_t err;
-  const bool half = layout == VIT_ROPE_HALF;
+  auto by_layout = [&](auto half_kernel, auto pair_kernel) { return layout == VIT_ROPE_HALF ? go(half_kernel) : go(pair_kernel); };
+  auto by_access = [&](auto t) {
+    using T = decltype(t);
+    constexpr int E = 16 / sizeof(T);
+    if (even >= E) return by_layout(rope_kernel<T, true, E>, rope_kernel<T, false, E>);
+    if (even >= E / 2) return by_layout(rope_kernel<T, true, E / 2>, rope_kernel<T, false, E / 2>);
+    return by_layout(rope_kernel<T, true, 1>, rope_kernel<T, false, 1>);
+  };
   if (type == VIT_DT_BF16)
-    err = half ? (vec ? go(rope_kernel<__nv_bfloat16, true, 8>) : go(rope_kernel<__nv_bfloat16, true, 1>))
-               : (vec ? go(rope_kernel<__nv_bfloat16, false, 8>) : go(rope_kernel<__nv_bfloat16, false, 1>));
+    err = by_access(__nv_bfloat16{});
   else if (type == VIT_DT_F16)
-    err = half ? (vec ? go(rope_kernel<__half, true, 8>) : go(rope_kernel<__half, true, 1>))
-               : (vec ? go(rope_kernel<__half, false, 8>) : go(rope_kernel<__half, false, 1>));
+    err = by_access(__half{});
   else
-    err = half ? (vec ? go(rope_kernel<float, true, 4>) : go(rope_kernel<float, true, 1>))
-               : (vec ? go(rope_kernel<float, false, 4>) : go(rope_kernel<float, false, 1>));
+    err = by_access(float{});
   CK(err);
   return VIT_OK;
 }
