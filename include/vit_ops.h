@@ -110,12 +110,13 @@ vit_status vit_op_rope(const vit_rope_tensor *q, const vit_rope_tensor *k, vit_d
  *   cu_q, cu_k: device int32 [n + 1], not decreasing; len_k: device int32 [n].  Read on the device
  *   (a captured call takes new lengths on replay); values outside the buffers are clamped.
  *   max_q: the longest query length if the caller knows it, 0 if not.  Only the choice of kernels
- *   goes by it (few query rows per sequence, as single tokens over a cache, run on a kernel that
- *   splits the keys' axis over the GPU): a wrong value costs time, not results.
+ *   goes by it, with n, Tk and the heads (few query rows over long key rows, as single tokens over a
+ *   cache, run on a kernel that splits the keys' axis over the GPU, short sequences on one without
+ *   shared memory): a wrong value costs time, not results.
  *   workspace: vit_op_attention_packed_workspace bytes of device memory, 16-byte aligned, that no
  *   other call uses before this one has run; needs no preparation.
  * Scores, softmax statistics and sums are fp32; the softmax weights are rounded to `type` for
- * the product with V (with few query rows: to twice its precision), the result once. */
+ * the product with V (few query rows or short sequences: to twice its precision), the result once. */
 typedef struct vit_attn_packed {
   const void *q, *k, *v;
   void *out;
@@ -130,8 +131,8 @@ typedef struct vit_attn_packed {
   size_t workspace_bytes;
 } vit_attn_packed;
 
-/* Workspace of a call with these arguments on the current device: 0 where none is used.  Depends on
- * max_q, heads_q, heads_k and head_dim (at most 10 MB), not on numbers of tokens or lengths. */
+/* Workspace of a call with these arguments on the current device: 0 where none is used, at most 10 MB.  Reads n,
+ * Tq, Tk, max_q, heads_q, heads_k, head_dim and type, no pointer. */
 vit_status vit_op_attention_packed_workspace(const vit_attn_packed *a, size_t *bytes);
 
 vit_status vit_op_attention_packed(const vit_attn_packed *a, vit_stream_t stream);

@@ -393,6 +393,25 @@ def check_attn(out, q, k, v, q0, k0, lq, lk, causal, scale, zmax=32.0):
         assert (err <= tol).all(), (b, lq[b], lk[b], (err - tol).max().item())
 
 
+KERNELS = ["tile", "split", "short"]
+
+
+def by_kernel(kernel, k, v, cu_q, cu_k, len_k=None):
+    """The arguments that make a call take the named kernel, without changing its result: key rows of nobody
+    (NaN) or empty sequences behind the others, and a max_q that need not be true."""
+    n = cu_q.shape[0] - 1
+    if kernel == "split":
+        pad = torch.full((600 * n, *k.shape[1:]), NAN, dtype=k.dtype, device="cuda")
+        return dict(k=torch.cat([k, pad]), v=torch.cat([v, pad]), cu_q=cu_q, cu_k=cu_k, len_k=len_k, max_q=1)
+    if kernel == "short":
+        more = max(0, -(-k.shape[0] // 64) - n)
+        cu_q, cu_k = (torch.cat([c, c[-1:].expand(more)]) for c in (cu_q, cu_k))
+        if len_k is not None:
+            len_k = torch.cat([len_k, torch.zeros(more, dtype=torch.int32, device="cuda")])
+        return dict(k=k, v=v, cu_q=cu_q, cu_k=cu_k, len_k=len_k, max_q=1)
+    return dict(k=k, v=v, cu_q=cu_q, cu_k=cu_k, len_k=len_k, max_q=0)
+
+
 LENS = {  # (query length, key length) of each sequence
     "one": [(1, 1)],
     "edges": [(1, 64), (64, 64), (65, 65), (63, 63), (127, 127), (128, 128), (129, 129), (2, 2)],
@@ -410,8 +429,8 @@ LENS = {  # (query length, key length) of each sequence
                                             (128, "bf16", 12, 1)])
 @pytest.mark.parametrize("lens", list(LENS))
 @pytest.mark.parametrize("causal", [True, False])
-@pytest.mark.parametrize("max_q", [0, "true", 1])
-def test_attention_packed(d, dtype, hq, hkv, lens, causal, max_q):
+@pytest.mark.parametrize("kernel", KERNELS + ["rule"])
+def test_attention_packed(d, dtype, hq, hkv, lens, causal, kernel):
     """Packed sequences behind one another, each followed by rows of nobody (NaN) that have to stay."""
     V = lib()
     lq, lk = [x[0] for x in LENS[lens]], [x[1] for x in LENS[lens]]
@@ -426,22 +445,23 @@ def test_attention_packed(d, dtype, hq, hkv, lens, causal, max_q):
     k[-tail:], v[-tail:], q[-tail:] = NAN, NAN, NAN
     out = torch.full((Tq, hq, d), 0.5, dtype=dt, device="cuda")
     cu_q, cu_k = cum(lq), cum(lk)
-    m = max(lq) if max_q == "true" else max_q
-    res = V.attention_packed(q, k, v, cu_q, cu_k, causal=causal, max_q=m, out=out)
+    args = dict(k=k, v=v, cu_q=cu_q, cu_k=cu_k, max_q=max(lq)) if kernel == "rule" else by_kernel(kernel, k, v, cu_q, cu_k)
+    res = V.attention_packed(q, **args, causal=causal, out=out)
     V.op_poll()
     assert res is out and (out[-tail:] == 0.5).all()
     check_attn(out, q, k, v, cu_q.tolist(), cu_k.tolist(), lq, lk, causal, d ** -0.5)
 
 
 @pytest.mark.parametrize("d,hq,hkv", [(64, 4, 2), (128, 8, 1), (128, 2, 2)])
-@pytest.mark.parametrize("max_q", [0, 1, 5])
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("single", [True, False])
 @pytest.mark.parametrize("room,lens", [(64, [1, 64, 0, 63]), (100, [100, 99, 65, 1, 64]), (1037, [1037, 3, 512, 1000])])
-def test_attention_over_a_cache(d, hq, hkv, max_q, room, lens):
+def test_attention_over_a_cache(d, hq, hkv, single, kernel, room, lens):
     """New tokens over caches with room, in a larger buffer with heads outside tokens: what lies past a length
     is NaN, queries of different numbers (none among them)."""
     V, g = lib(), gen(room)
     n = len(lens)
-    lq = [min(lens[i], (1, 3, 0, 5, 2)[i]) if max_q != 1 else 1 for i in range(n)]
+    lq = [1 if single else min(lens[i], (1, 3, 0, 5, 2)[i]) for i in range(n)]
     Tk = n * room + 7
     kv = randn(g, 2, hkv, Tk, d, dtype=torch.bfloat16)
     for i, ln in enumerate(lens):
@@ -452,7 +472,7 @@ def test_attention_over_a_cache(d, hq, hkv, max_q, room, lens):
     out = torch.full_like(q, 0.5)
     cu_q, cu_k = cum(lq), cum([room] * n)
     len_k = torch.tensor(lens, dtype=torch.int32, device="cuda")
-    V.attention_packed(q, k, v, cu_q, cu_k, len_k=len_k, causal=True, scale=0.2, max_q=max_q, out=out)
+    V.attention_packed(q, **by_kernel(kernel, k, v, cu_q, cu_k, len_k), causal=True, scale=0.2, out=out)
     V.op_poll()
     check_attn(out, q, k, v, cu_q.tolist(), cu_k.tolist(), lq, lens, True, 0.2)
     assert (out[sum(lq):] == 0.5).all()
@@ -475,12 +495,12 @@ def test_attention_tokens_long_cache(n, hq, hkv, d, lk, dtype):
 
 
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("max_q", [0, 1])
-def test_attention_sharp_and_large_scores(d, max_q):
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_attention_sharp_and_large_scores(d, kernel):
     """Scores that grow along the keys by far more than the rescaling step, up to 1e6, and a sink that takes all
     the weight."""
     V, g = lib(), gen(d)
-    lk, lq = 700, 130 if max_q == 0 else 1
+    lk, lq = 700, 130
     q = torch.ones(lq, 2, d, device="cuda", dtype=torch.bfloat16)
     k = torch.zeros(lk, 2, d, device="cuda", dtype=torch.bfloat16)
     # exact in bf16 and fp32: scores 0, 64, 128, ... on every 50th key; the second head falls instead
@@ -489,31 +509,31 @@ def test_attention_sharp_and_large_scores(d, max_q):
     v = randn(g, lk, 2, d, dtype=torch.bfloat16)
     cu_q, cu_k = cum([lq]), cum([lk])
     for causal in (False, True):
-        out = V.attention_packed(q, k, v, cu_q, cu_k, causal=causal, scale=1.0, max_q=max_q)
+        out = V.attention_packed(q, **by_kernel(kernel, k, v, cu_q, cu_k), causal=causal, scale=1.0)
         check_attn(out, q, k, v, [0], [0], [lq], [lk], causal, 1.0, zmax=1.0)
     k[:, :, 0] = 0
     k[123, :, 0] = 1.0e6
-    out = V.attention_packed(q, k, v, cu_q, cu_k, scale=1.0, max_q=max_q)
+    out = V.attention_packed(q, **by_kernel(kernel, k, v, cu_q, cu_k), scale=1.0)
     # one weight, rounded (u), over an unrounded or rounded sum, and the result's rounding
     assert ((out.double() - v[123].double()).abs() <= 2.02 * 2.0 ** -8 * v[123].double().abs()).all()
     V.op_poll()
 
 
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("max_q", [0, 1])
+@pytest.mark.parametrize("kernel", KERNELS)
 @pytest.mark.parametrize("at", range(60, 80))
-def test_attention_nan_and_infinite_keys(d, max_q, at):
+def test_attention_nan_and_infinite_keys(d, kernel, at):
     """A NaN in a key, or a score of +infinity, reaches exactly the rows that see it; -infinity is weight 0."""
     V, g = lib(), gen(at)
     n = 150
     q, k, v = (randn(g, n, 2, d, dtype=torch.bfloat16) for _ in range(3))
     q[..., 0] = q[..., 0].abs() + 0.1
     cu = cum([n])
-    clean = V.attention_packed(q, k, v, cu, cu, causal=True, max_q=max_q)
+    clean = V.attention_packed(q, **by_kernel(kernel, k, v, cu, cu), causal=True)
     for bad in (NAN, math.inf, -math.inf):
         k2 = k.clone()
         k2[at, 0, 0] = bad
-        out = V.attention_packed(q, k2, v, cu, cu, causal=True, max_q=max_q)
+        out = V.attention_packed(q, **by_kernel(kernel, k2, v, cu, cu), causal=True)
         assert torch.equal(out[:at], clean[:at]) and torch.equal(out[:, 1], clean[:, 1])
         if bad == -math.inf:
             assert torch.isfinite(out.float()).all()
@@ -522,26 +542,28 @@ def test_attention_nan_and_infinite_keys(d, max_q, at):
     V.op_poll()
 
 
-@pytest.mark.parametrize("max_q", [0, 1])
-def test_attention_clamps_bad_bounds(max_q):
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_attention_clamps_bad_bounds(kernel):
     """Bounds outside the buffers (stale tables) read and write nothing outside them; a length past a
     sequence's room is its room."""
     V, g = lib(), gen(20)
+    keys = 2000 if kernel == "split" else 90
     q = randn(g, 6, 2, 64, dtype=torch.bfloat16)
-    k, v = randn(g, 90, 2, 64, dtype=torch.bfloat16), randn(g, 90, 2, 64, dtype=torch.bfloat16)
+    k, v = randn(g, keys, 2, 64, dtype=torch.bfloat16), randn(g, keys, 2, 64, dtype=torch.bfloat16)
     cu_q = torch.tensor([0, 1, 2, 999], dtype=torch.int32, device="cuda")
     cu_k = torch.tensor([-50, 30, 60, 100000], dtype=torch.int32, device="cuda")
     len_k = torch.tensor([500, 30, -3], dtype=torch.int32, device="cuda")
-    out = V.attention_packed(q, k, v, cu_q, cu_k, len_k=len_k, max_q=max_q)
+    out = V.attention_packed(q, k, v, cu_q, cu_k, len_k=len_k, max_q=0 if kernel == "tile" else 1)
     V.op_poll()
     check_attn(out, q, k, v, [0, 1, 2], [0, 30, 60], [1, 1, 4], [30, 30, 0], False, 0.125)
 
 
-@pytest.mark.parametrize("max_q", [0, 1])
-def test_attention_streams_and_two_captured_graphs(max_q):
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_attention_streams_and_two_captured_graphs(kernel):
     """Calls side by side on two streams, and two captured graphs replayed side by side with new lengths."""
     V, g = lib(), gen(21)
-    n, hq, hkv, d, room = 9, 8, 2, 128, 600
+    n, hq, hkv, d, room = 9, 8, 2, 128, 60 if kernel == "short" else 600
+    max_q = 0 if kernel == "tile" else 1
     lens = [[(37 * i + s) % room + 1 for i in range(n)] for s in (1, 200, 411)]
     work = []
     for s in range(2):

@@ -248,15 +248,16 @@ def test_rope_frequency_refusals(kw, expect):
 @pytest.mark.parametrize("kw", [dict(workspace=None, workspace_bytes=1 << 30), dict(workspace=A, workspace_bytes=64),
                                 dict(workspace=A + 8, workspace_bytes=1 << 30)])
 def test_attention_workspace_refusals(kw):
-    """Few query rows per sequence take a workspace: refused where it is missing, too small or misaligned."""
-    assert ops._fn("attention_packed")(ctypes.byref(attn_args(max_q=1, **kw)), None) == V.VIT_E_WORKSPACE
+    """Few query rows over long key rows take a workspace: refused where it is missing, too small or misaligned."""
+    assert ops._fn("attention_packed")(ctypes.byref(attn_args(max_q=1, Tk=4096, **kw)), None) == V.VIT_E_WORKSPACE
 
 
 def test_attention_workspace_size():
     need = ctypes.c_size_t(7)
     f = ops._fn("attention_packed_workspace")
     assert f(ctypes.byref(attn_args(max_q=0)), need) == V.VIT_OK and need.value == 0
-    assert f(ctypes.byref(attn_args(max_q=1)), need) == V.VIT_OK and 0 < need.value <= 10 << 20
-    assert f(ctypes.byref(attn_args(max_q=1, head_dim=128)), need) == V.VIT_OK and 0 < need.value <= 10 << 20
+    assert f(ctypes.byref(attn_args(max_q=1)), need) == V.VIT_OK and need.value == 0
+    assert f(ctypes.byref(attn_args(max_q=1, Tk=4096)), need) == V.VIT_OK and 0 < need.value <= 10 << 20
+    assert f(ctypes.byref(attn_args(max_q=1, Tk=4096, head_dim=128)), need) == V.VIT_OK and 0 < need.value <= 10 << 20
     assert f(ctypes.byref(attn_args(max_q=1, head_dim=80)), need) == V.VIT_E_UNSUPPORTED
     assert f(ctypes.byref(attn_args(max_q=1)), None) == V.VIT_E_INVALID_ARG

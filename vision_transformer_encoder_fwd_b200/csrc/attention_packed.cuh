@@ -67,9 +67,10 @@ __device__ __forceinline__ void seq_bounds(const AttnPackedParams& p, int i, Seq
   if (p.len_k != nullptr) s.lk = clampi(p.len_k[i], 0, s.lk);
 }
 
-// Finds tile number `want` in the order of the sequences, ceil(lq / bm) tiles each.  One warp; every lane gets the answer.  Each round takes 128 sequences, four
+// Finds tile number `want` in the order of the sequences, ceil(lq * mul / bm) tiles each.  One warp; every lane gets the answer.  Each round takes 128 sequences, four
 // per lane, so that up to that many cost one trip to memory.  seq = -1: there is no such tile.
-__device__ __forceinline__ SeqTile find_tile(const AttnPackedParams& p, int want, int bm) {
+__device__ __forceinline__ SeqTile find_tile(const AttnPackedParams& p, int want, int bm,
+                                             int mul = 1) {
   const int lane = threadIdx.x & 31;
   SeqTile s;
   s.seq = -1;
@@ -81,7 +82,7 @@ __device__ __forceinline__ SeqTile find_tile(const AttnPackedParams& p, int want
     int cnt[4], sum = 0;
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      cnt[u] = (base + lane * 4 + u < p.n) ? (max(0, c[u + 1] - c[u]) + bm - 1) / bm : 0;
+      cnt[u] = (base + lane * 4 + u < p.n) ? (max(0, c[u + 1] - c[u]) * mul + bm - 1) / bm : 0;
       sum += cnt[u];
     }
     int incl = sum;

@@ -6,6 +6,7 @@
 #include "../../include/vit_ops.h"
 #include "attention_packed.cuh"
 #include "attention_rows.cuh"
+#include "attention_short.cuh"
 #include "host_common.cuh"
 #include "linear_fp8.cuh"
 #include "rope.cuh"
@@ -271,11 +272,30 @@ cudaError_t launch_attn_packed(const CUtensorMap& q, const CUtensorMap& k, const
                     dim3(ATT_THREADS), smem, s, q, k, v, p, st);
 }
 
-// Few query rows per sequence (max_q queries of the heads that share a key head) go to the row kernel.
-constexpr int64_t kRowsKernelMax = 64;
-bool takes_rows_kernel(const vit_attn_packed* a) {
+// Which kernel a call takes.  Lengths are on the device: the rule goes by max_q and the key rows there are
+// for a sequence on average (a cache's room).  Measured on a B200, us: short / split / tile kernel, for
+// sequences x queries x keys, heads on key heads x width:
+//   150 x 24 x 24, 16 on 16 x 64     11 / 29 / 52      74 x 24 x 24, 32 on 8 x 128    15 / 41 / 19
+//   100 x 96 x 96, 16 on 16 x 64     40 / 64 / 50      74 x 48 x 48, 32 on 8 x 128    40 / 75 / 35
+//   40 x 128 x 128, 16 on 16 x 64    25 / 39 / 24      57 x 48 x 48, 16 on 4 x 64      9 / 30 / 12
+//   64 x 1 x 64, 32 on 8 x 128      7.3 / 11 / 12      8 x 1 x 128, 32 on 8 x 128    9.0 / 8.3 / 6.4
+//   64 x 1 x 128                     13 / 13 / 14      8 x 1 x 512                    28 / 12 / 10
+//   64 x 1 x 512                     46 / 33 / 31      8 x 1 x 2048                  153 / 22 / 28
+//   300 x 1 x 100, 8 on 1 x 64      7.8 / 11 / 13      96 x 1 x 512, 16 on 16 x 64    52 / 51 / 64
+enum AttnKernel { ATTN_TILE, ATTN_SPLIT, ATTN_SHORT };
+AttnKernel attention_kernel(const vit_attn_packed* a) {
   const int64_t group = a->heads_q / a->heads_k;
-  return a->max_q > 0 && a->max_q * group <= kRowsKernelMax && a->Tq * group <= 0x7fffffffLL;
+  const int64_t rows = a->max_q * group;
+  if (a->max_q <= 0 || a->n == 0 || a->Tq * group > 0x7fffffffLL) return ATTN_TILE;
+  const int64_t keys = a->Tk / a->n;
+  const int64_t work = static_cast<int64_t>(a->n) * a->heads_k;  // sequences and key heads
+  const bool many = work > 2 * current_sms();
+  // the short kernel: 16 x 16 blocks of one warp
+  const int64_t blocks = (rows + 15) / 16 * ((keys + 15) / 16);
+  if (blocks <= (a->head_dim == 64 ? 36 : 24) && (keys <= 64 || (keys <= 128 && many)) && a->heads_k <= 65535)
+    return ATTN_SHORT;
+  if (rows > 64 || (keys <= 512 && work <= 4 * current_sms())) return ATTN_TILE;
+  return ATTN_SPLIT;
 }
 
 template <int HD>
@@ -302,6 +322,15 @@ cudaError_t launch_attn_rows(const CUtensorMap& k, const CUtensorMap& v, const A
   e = launch_pdl(attn_rows_kernel<T, HD>, dim3(pieces), dim3(ATTR_THREADS), smem, s, k, v, p, st);
   if (e != cudaSuccess || pieces == 1) return e;
   return launch_pdl(attn_join_kernel<T, HD>, dim3(pieces - 1), dim3(128), 0, s, p, pieces, st);
+}
+
+template <typename T, int HD>
+cudaError_t launch_attn_short(const AttnPackedParams& a, int* st, cudaStream_t s) {
+  const AttnShortParams p{a, fast_div(static_cast<uint32_t>(a.Hq / a.Hkv))};
+  const int64_t tiles = static_cast<int64_t>(a.Tq) * p.group.d / 16 + a.n;  // at most as many
+  return launch_pdl(attn_short_kernel<T, HD>,
+                    dim3(static_cast<unsigned>((tiles + ATTS_WARPS - 1) / ATTS_WARPS), static_cast<unsigned>(a.Hkv)),
+                    dim3(32 * ATTS_WARPS), 0, s, p, st);
 }
 
 vit_status check_attention(const vit_attn_packed* a) {
@@ -516,7 +545,7 @@ vit_status vit_op_attention_packed_workspace(const vit_attn_packed* a, size_t* b
   const vit_status st = check_attention(a);
   if (st != VIT_OK) return st;
   if (!bytes) return fail(VIT_E_INVALID_ARG, "bytes is NULL");
-  *bytes = takes_rows_kernel(a) ? rows_workspace(a->head_dim) : 0;
+  *bytes = attention_kernel(a) == ATTN_SPLIT ? rows_workspace(a->head_dim) : 0;
   return VIT_OK;
 }
 
@@ -534,7 +563,8 @@ vit_status vit_op_attention_packed(const vit_attn_packed* a, vit_stream_t stream
   for (int64_t s : strides)
     if (s % 8 || s < 0 || s >= (1LL << 38)) return fail(VIT_E_SHAPE, "strides must be multiples of 8, not negative");
   if (static_cast<int64_t>(a->n) + a->Tq > 0x7fffffffLL) return fail(VIT_E_SHAPE, "too many sequences");
-  const bool rows = takes_rows_kernel(a);
+  const AttnKernel which = attention_kernel(a);
+  const bool rows = which == ATTN_SPLIT;
   if (rows && (!a->workspace || !aligned16(a->workspace) || a->workspace_bytes < rows_workspace(a->head_dim)))
     return fail(VIT_E_WORKSPACE, "workspace missing, not 16-byte aligned or too small");
   AttnPackedParams p{};
@@ -567,6 +597,18 @@ vit_status vit_op_attention_packed(const vit_attn_packed* a, vit_stream_t stream
   for (int x = 2; x <= std::min(group, 128); ++x)
     if (group % x == 0 && 128 / x * x >= 120) p.pack = x;
   p.tokens = 128 / p.pack;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (which == ATTN_SHORT) {
+    if (a->type == VIT_DT_BF16)
+      e = a->head_dim == 64 ? launch_attn_short<__nv_bfloat16, 64>(p, a->status, s)
+                            : launch_attn_short<__nv_bfloat16, 128>(p, a->status, s);
+    else
+      e = a->head_dim == 64 ? launch_attn_short<__half, 64>(p, a->status, s)
+                            : launch_attn_short<__half, 128>(p, a->status, s);
+    CK(e);
+    return VIT_OK;
+  }
   CUtensorMap tq, tk, tv;
   // without keys nothing is loaded: any valid map will do
   const void* kb = a->Tk > 0 ? a->k : a->q;
@@ -576,8 +618,6 @@ vit_status vit_op_attention_packed(const vit_attn_packed* a, vit_stream_t stream
       !tmap_heads(&tk, kb, a->head_dim, a->heads_k, tkeys, a->k_head, a->k_token, 64) ||
       !tmap_heads(&tv, vb, a->head_dim, a->heads_k, tkeys, a->v_head, a->v_token, 64))
     return no_map();
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e;
   if (rows) {
     if (a->type == VIT_DT_BF16)
       e = a->head_dim == 64 ? launch_attn_rows<__nv_bfloat16, 64>(tk, tv, p, a->max_q, a->workspace, a->status, s)

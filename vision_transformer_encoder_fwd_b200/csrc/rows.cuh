@@ -119,7 +119,7 @@ struct RowsParams {
 // per thread, vector v of thread t at element (v * tpr + t) * E.
 // RMODE: 0 no residual, 1 residual of x's type, 2 fp32 residual.
 template <typename TX, int RMODE, bool OUT8, int E, int NV>
-__global__ void __launch_bounds__(E == 8 && NV < 4 ? 512 : 1024, E == 8 && NV < 4 ? (RMODE == 1 ? 3 : 2) : 1) rows_kernel(RowsParams p, int tpr) {
+__global__ void __launch_bounds__(E == 8 && NV < 4 ? 512 : 1024, E == 8 && NV < 4 ? (RMODE == 1 ? 3 : 2) : NV == 8 ? 2 : 1) rows_kernel(RowsParams p, int tpr) {
   using TR = typename std::conditional<RMODE == 2, float, TX>::type;
   constexpr bool VEC = E > 1;
   __shared__ float2 part[32];
