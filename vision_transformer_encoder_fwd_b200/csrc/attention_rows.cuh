@@ -503,22 +503,32 @@ __global__ void __launch_bounds__(ATTR_THREADS, AttnRowsCfg<HD>::PER_SM)
 }
 
 // Joins the partial results of the items that piece boundaries cut.  CTA b looks at the boundary
-// between pieces b and b + 1 and takes the item there, if that is the first boundary in it.
+// between pieces b and b + 1 and takes the item there, if that is the first boundary in it.  Its 16
+// warps share the item's rows, and several of them a row's parts: one long sequence leaves few items of
+// very many parts (8 items of 37 parts took 20 us with a thread's loop over all parts).
+constexpr int ATTJ_WARPS = 16;
+
 template <typename T, int HD>
-__global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ AttnRowsParams pr, int pieces, int* status) {
+__global__ void __launch_bounds__(32 * ATTJ_WARPS) attn_join_kernel(const __grid_constant__ AttnRowsParams pr, int pieces,
+                                                                    int* status) {
+  constexpr int V = HD / 32;  // values a lane
   const AttnPackedParams& p = pr.a;
-  __shared__ long long s_at[4];
+  __shared__ long long s_at[3];
   __shared__ int s_seq;
+  // half of the warps' sums: with no more than this the CTA fits beside two of the kernel ahead
+  __shared__ float s_o[ATTJ_WARPS / 2][HD];
+  __shared__ float s_l[ATTJ_WARPS / 2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int group = static_cast<int>(pr.group.d);
   // the lengths were there before the kernel ahead began: only its results have to be waited for
-  if (threadIdx.x < 32) {
+  if (warp == 0) {
     int seq;
     long long base, per = 0, at = 0;
     rows_scan(p, group, [&](long long total) {
       per = max(static_cast<long long>(ATTR_MIN_UNITS), (total + pieces - 1) / pieces);
       return at = per * (blockIdx.x + 1);
     }, seq, base);
-    if (threadIdx.x == 0) {
+    if (lane == 0) {
       s_seq = seq;
       s_at[0] = at;
       s_at[1] = base;
@@ -542,38 +552,64 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ 
   const int odd = u0 > c0 * per ? 1 : 0;
   const int hk = static_cast<int>(item / nt);
   const int row0 = static_cast<int>(item - hk * nt) * 16;
-  const int rows = s.lq * group;
-  const int off = s.lk - s.lq;
+  const int nrows = min(16, s.lq * group - row0);
+  int share = 1;  // warps a row
+  while (share * 2 * nrows <= ATTJ_WARPS) share *= 2;
+  const int row = warp / share, part = warp % share;
   const float c = p.scale_log2;
-  for (int i = threadIdx.x; i < 16 * (HD / 4); i += 128) {
-    const int row = i / (HD / 4), ch = i % (HD / 4);
-    const int arow = row0 + row;
-    if (arow >= rows) break;
+  const bool work = row < nrows;
+  auto slot = [&](int x) { return (2 * x + (x == c0 ? odd : 0)) * 16 + row; };
+  float v[V], sum = 0.f;
+#pragma unroll
+  for (int e = 0; e < V; ++e) v[e] = 0.f;
+  if (work) {
     float top = -INFINITY;
+    for (int x = c0 + lane; x <= c1; x += 32) top = maxn(top, pr.part_ml[slot(x)].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = maxn(top, __shfl_xor_sync(0xffffffffu, top, o));
 #pragma unroll 4
-    for (int x = c0; x <= c1; ++x) top = maxn(top, pr.part_ml[(2 * x + (x == c0 ? odd : 0)) * 16 + row].x);
-    float sum = 0.f;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int x = c0; x <= c1; ++x) {
-      const int64_t at_row = (2 * x + (x == c0 ? odd : 0)) * 16 + row;
-      const float2 ml = pr.part_ml[at_row];
-      const float4 a = *reinterpret_cast<const float4*>(pr.part_o + at_row * HD + ch * 4);
+    for (int x = c0 + part; x <= c1; x += share) {
+      const float2 ml = pr.part_ml[slot(x)];
+      const float* src = pr.part_o + static_cast<int64_t>(slot(x)) * HD + lane * V;
       const float w = to_max(ml.x, top, c);
-      sum += ml.y * w;
-      v.x += a.x * w;
-      v.y += a.y * w;
-      v.z += a.z * w;
-      v.w += a.w * w;
+      sum = fmaf(ml.y, w, sum);
+      float a[V];
+      if constexpr (V == 4) {
+        const float4 q = *reinterpret_cast<const float4*>(src);
+        a[0] = q.x, a[1] = q.y, a[2] = q.z, a[3] = q.w;
+      } else {
+        const float2 q = *reinterpret_cast<const float2*>(src);
+        a[0] = q.x, a[1] = q.y;
+      }
+#pragma unroll
+      for (int e = 0; e < V; ++e) v[e] = fmaf(a[e], w, v[e]);
     }
-    const int t = div_by(arow, pr.group);
-    const bool sees = (p.causal ? min(s.lk, t + off + 1) : s.lk) > 0;
-    const float inv = sees ? 1.0f / sum : 0.f;
-    T* dst = static_cast<T*>(p.out) + static_cast<int64_t>(s.q0 + t) * p.o_tok +
-             static_cast<int64_t>(hk * group + arow - t * group) * p.o_head + ch * 4;
-    *reinterpret_cast<uint2*>(dst) = sees ? make_uint2(pack2<T>(v.x * inv, v.y * inv), pack2<T>(v.z * inv, v.w * inv))
-                                          : make_uint2(0u, 0u);
   }
+  for (int h = share / 2; h > 0; h /= 2) {  // the upper half of a row's warps hands its sums to the lower
+    const int at_s = row * h + (part & (h - 1));
+    if (work && part >= h && part < 2 * h) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) s_o[at_s][lane * V + e] = v[e];
+      if (lane == 0) s_l[at_s] = sum;
+    }
+    __syncthreads();
+    if (work && part < h) {
+      sum += s_l[at_s];
+#pragma unroll
+      for (int e = 0; e < V; ++e) v[e] += s_o[at_s][lane * V + e];
+    }
+    __syncthreads();
+  }
+  if (!work || part != 0) return;
+  const int arow = row0 + row;
+  const int t = div_by(arow, pr.group);
+  const bool sees = (p.causal ? min(s.lk, t + s.lk - s.lq + 1) : s.lk) > 0;
+  const float inv = sees ? 1.0f / sum : 0.f;
+  T* dst = static_cast<T*>(p.out) + static_cast<int64_t>(s.q0 + t) * p.o_tok +
+           static_cast<int64_t>(hk * group + arow - t * group) * p.o_head + lane * V;
+#pragma unroll
+  for (int e = 0; e < V; e += 2)
+    reinterpret_cast<uint32_t*>(dst)[e / 2] = sees ? pack2<T>(v[e] * inv, v[e + 1] * inv) : 0u;
 }
 
 }  // namespace vit

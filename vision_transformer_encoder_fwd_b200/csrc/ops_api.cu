@@ -177,7 +177,8 @@ bool tmap_heads(CUtensorMap* tm, const void* base, int d, int heads, int64_t tok
   cuuint32_t box[3] = {64, box_heads, box_tokens};
   cuuint32_t estr[3] = {1, 1, 1};
   return fn(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, d == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -321,7 +322,7 @@ cudaError_t launch_attn_rows(const CUtensorMap& k, const CUtensorMap& v, const A
   p.part_ml = reinterpret_cast<float2*>(p.part_o + static_cast<size_t>(pieces) * 2 * 16 * HD);
   e = launch_pdl(attn_rows_kernel<T, HD>, dim3(pieces), dim3(ATTR_THREADS), smem, s, k, v, p, st);
   if (e != cudaSuccess || pieces == 1) return e;
-  return launch_pdl(attn_join_kernel<T, HD>, dim3(pieces - 1), dim3(128), 0, s, p, pieces, st);
+  return launch_pdl(attn_join_kernel<T, HD>, dim3(pieces - 1), dim3(32 * ATTJ_WARPS), 0, s, p, pieces, st);
 }
 
 template <typename T, int HD>
