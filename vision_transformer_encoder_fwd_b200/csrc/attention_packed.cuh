@@ -196,10 +196,11 @@ struct AttnPackedCfg {
   static_assert(8 * (UNITS + 2 * DONE + 4) + 8 + 8 * 4 <= 512, "barrier area");
 };
 
-// 2^x for a pair on the FMA pipe, as exp2_fma2, with a NaN kept (the clamp and the last step let it through).
-__device__ __forceinline__ float2 exp2_fma2_nan(float2 x) {
-  x.x = max_nan(x.x, -125.0f);
-  x.y = max_nan(x.y, -125.0f);
+// 2^x for a pair on the FMA pipe, as exp2_fma2, but with a NaN kept and exactly 0 from -126.5 down: the clamp
+// gives j = -127, whose power of two has no exponent bits.
+__device__ __forceinline__ float2 exp2_fma2_full(float2 x) {
+  x.x = max_nan(x.x, -127.0f);
+  x.y = max_nan(x.y, -127.0f);
   const float2 t = fadd2(x, make_float2(12582912.0f, 12582912.0f));
   const float2 j = fadd2(t, make_float2(-12582912.0f, -12582912.0f));
   const float2 f = fadd2(x, make_float2(-j.x, -j.y));
@@ -211,15 +212,11 @@ __device__ __forceinline__ float2 exp2_fma2_nan(float2 x) {
   return ffma2(p, two_j, make_float2(0.f, 0.f));
 }
 
-// Every PACKED_POLY-th pair of exponentials goes to the FMA pipe.
-#ifndef PACKED_POLY
-#define PACKED_POLY 8
-#endif
-
 // P for 64 keys of one row: 2^(s c - mc), rounded, into 32 columns of tensor memory; with SUM returns the
-// sum of the unrounded values.  Masked scores are -infinity.
-template <typename T, bool MASK, bool SUM>
-__device__ __forceinline__ float packed_p64(const float (&s)[64], float c, float mc, int valid, uint32_t t_p) {
+// sum of the unrounded values.  Masked scores are -infinity.  Every POLY-th pair of exponentials goes to the
+// FMA pipe (4th at width 64, 8th at 128: 2nd to 16th were within 5 %, the 2nd slowest).
+template <typename T, bool SUM, int POLY>
+__device__ __forceinline__ float packed_p64(const float (&s)[64], float c, float mc, uint32_t t_p) {
   const float2 cc = make_float2(c, c);
   const float2 nm = make_float2(-mc, -mc);
   float2 l0 = make_float2(0.f, 0.f), l1 = l0;
@@ -231,15 +228,10 @@ __device__ __forceinline__ float packed_p64(const float (&s)[64], float c, float
       const int t = b * 32 + u * 2;
       const float2 x = ffma2(make_float2(s[t], s[t + 1]), cc, nm);
       float2 e;
-      if ((t >> 1) % PACKED_POLY == PACKED_POLY - 1) {
-        e = exp2_fma2_nan(x);
-        if (MASK) {
-          e.x = (t < valid) ? e.x : 0.f;
-          e.y = (t + 1 < valid) ? e.y : 0.f;
-        }
-      } else {
+      if ((t >> 1) % POLY == POLY - 1)
+        e = exp2_fma2_full(x);
+      else
         e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-      }
       if (SUM) {
         if (u & 1)
           l1 = fadd2(l1, e);
@@ -291,8 +283,8 @@ __global__ void __launch_bounds__(ATT_THREADS, AttnPackedCfg<HD>::PER_SM)
       mbar_init(&s_done[s], 1);
       mbar_init(&pv_done[s], 1);
     }
-    mbar_init(&p_full[0], 128);
-    mbar_init(&p_full[1], 128);
+    mbar_init(&p_full[0], 4);  // a warp's lanes arrive as one
+    mbar_init(&p_full[1], 4);
     mbar_init(mma_done, 1);
     fence_mbar_init();
     tma_prefetch_desc(&tmQ);
@@ -435,6 +427,7 @@ __global__ void __launch_bounds__(ATT_THREADS, AttnPackedCfg<HD>::PER_SM)
     const uint32_t t_o = tmem_base + lane_off + Cfg::TM_O;
     // keys this row sees (<= 0: none); rows of nobody go along with the last one
     const int lim = p.causal ? min(st.lk, min(tok, st.lq - 1) + off + 1) : st.lk;
+    const int whole = __reduce_min_sync(0xffffffffu, max(lim, 0)) / 64;  // blocks that every row of the warp sees whole
     const float c = p.scale_log2;
     float m = -INFINITY, l = 0.f;
     bool ok = true;
@@ -449,9 +442,8 @@ __global__ void __launch_bounds__(ATT_THREADS, AttnPackedCfg<HD>::PER_SM)
       float s[64];
       __syncwarp();
       tmem_ld64(t_b, s);
-      const int valid = lim - n * 64;
-      const bool part = __any_sync(0xffffffffu, valid < 64);
-      if (part) {
+      if (__builtin_expect(n >= whole, 0)) {
+        const int valid = lim - n * 64;
 #pragma unroll
         for (int t = 0; t < 64; ++t) s[t] = (t < valid) ? s[t] : -INFINITY;
       }
@@ -463,7 +455,7 @@ __global__ void __launch_bounds__(ATT_THREADS, AttnPackedCfg<HD>::PER_SM)
         m = m_new;
         l *= alpha;
       }
-      if (n > 0 && __any_sync(0xffffffffu, resc)) {
+      if (__builtin_expect(n > 0 && __any_sync(0xffffffffu, resc), 0)) {
         if (!wait_warp(smem_u32(pv_done) + ((n - 1) % DONE) * 8, static_cast<uint32_t>((n - 1) / DONE) & 1u, abort_flag, gstatus,
                        DEV_TIMEOUT_ATTP + 8, wlim)) {
           ok = false;
@@ -480,7 +472,7 @@ __global__ void __launch_bounds__(ATT_THREADS, AttnPackedCfg<HD>::PER_SM)
           tmem_st16(t_o + u, ob);
         }
       }
-      if (n == nblk - 1 && st.lk < nblk * 64) {
+      if (__builtin_expect(n == nblk - 1 && st.lk < nblk * 64, 0)) {
         // V rows past the sequence's keys: zeros
         const int pos = pos_v(n);
         if (!wait_warp(smem_u32(&full[pos % UNITS]), static_cast<uint32_t>(pos / UNITS) & 1u, abort_flag, gstatus,
@@ -497,10 +489,11 @@ __global__ void __launch_bounds__(ATT_THREADS, AttnPackedCfg<HD>::PER_SM)
       }
       const float mc = max_offset(m, c);
       __syncwarp();
-      l += part ? packed_p64<T, true, !Cfg::ONES>(s, c, mc, valid, t_b) : packed_p64<T, false, !Cfg::ONES>(s, c, mc, valid, t_b);
+      l += packed_p64<T, !Cfg::ONES, HD == 64 ? 4 : 8>(s, c, mc, t_b);
       tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(&p_full[n & 1]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[n & 1]);
     }
     if (ok && nblk > 0) ok = wait_warp(smem_u32(mma_done), 0, abort_flag, gstatus, DEV_TIMEOUT_ATTP + 10, wlim);
     if (ok) {
