@@ -92,13 +92,11 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return d;
 }
 
-// The scale of a row whose largest magnitude is `amax`, and what its values are multiplied by: both within two
-// units in the last place (two IEEE divisions were a third of a thread's instructions in a row).
-__device__ __forceinline__ float row_scale(float amax, float& mul) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(amax));
-  mul = kE4m3Max * r;
-  return amax * (1.0f / kE4m3Max);
+// What the values v = h w of a row are multiplied by on their way to 8 bits: rstd / s with s = top rstd / 448, so
+// that rstd drops out and only the quotient is rounded.  `amax` is top rstd; below the smallest one the
+// scale is that one's.
+__device__ __forceinline__ float row_factor(float top, float rstd, float amax) {
+  return amax <= kRowAmaxMin ? rstd * (kE4m3Max / kRowAmaxMin) : kE4m3Max / top;
 }
 
 struct RowsParams {
@@ -188,17 +186,18 @@ __global__ void __launch_bounds__(E == 8 && NV < 4 ? 512 : 1024, E == 8 && NV < 
   }
   if (!live) return;
   const float rstd = norm ? rsqrtf(ss / static_cast<float>(p.D) + p.eps) : 1.0f;
-  float mul = 1.0f;  // on top of rstd: their product could overflow where the values do not
+  float mul = rstd;
   if (OUT8) {
-    const float scale = row_scale(max_nan(top * rstd, kRowAmaxMin), mul);
-    if (t == 0) p.scales[row] = scale;
+    const float amax = top * rstd;
+    mul = row_factor(top, rstd, amax);
+    if (t == 0) p.scales[row] = max_nan(amax, kRowAmaxMin) / kE4m3Max;
   }
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
     const int c = (v * tpr + t) * E;
     if (c >= p.D) continue;
 #pragma unroll
-    for (int i = 0; i < E; ++i) h[v][i] = h[v][i] * rstd * mul;
+    for (int i = 0; i < E; ++i) h[v][i] *= mul;
     if (OUT8) {
       uint8_t* o = static_cast<uint8_t*>(p.out) + row * p.out_ld + c;
       if constexpr (E == 8) {
@@ -300,17 +299,18 @@ __global__ void __launch_bounds__(512) rows_stream_kernel(RowsParams p, int tpr)
       flip ^= 1;
     }
     const float rstd = norm ? rsqrtf(ss / static_cast<float>(p.D) + p.eps) : 1.0f;
-    float mul = 1.0f;  // on top of rstd, as above
+    float mul = rstd;
     if (OUT8) {
-      const float scale = row_scale(max_nan(top * rstd, kRowAmaxMin), mul);
-      if (t == 0) p.scales[row] = scale;
+      const float amax = top * rstd;
+      mul = row_factor(top, rstd, amax);
+      if (t == 0) p.scales[row] = max_nan(amax, kRowAmaxMin) / kE4m3Max;
     }
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int c = (v * tpr + t) * 8;
       if (c >= p.D) continue;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) h[v][i] = OUT8 ? h[v][i] * rstd * mul : h[v][i] * rstd;
+      for (int i = 0; i < 8; ++i) h[v][i] *= mul;
       if (OUT8)
         *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out) + row * p.out_ld + c) =
             make_uint2(e4m3x2(h[v][0], h[v][1]) | e4m3x2(h[v][2], h[v][3]) << 16,
