@@ -672,10 +672,9 @@ __global__ void __launch_bounds__(LIN8_THREADS, 1)
 // ------------------------------------------------------------------------------------------------
 // Few rows of A (new tokens): the weights' bytes bound it, so they are read once, by all SMs, straight
 // from global memory into mma.sync fragments.  A CTA takes 16 rows of W (the M side of m16n8k32) and
-// NB groups of 8 rows of A (the N side); its 8 warps split K and are joined through shared memory
-// in a fixed order.  The order of K inside a 64-byte chunk is free as long as both sides share it, so a
+// NB groups of 8 rows of A (the N side); its warps split K and are joined through shared memory in a
+// fixed order.  The order of K inside a 64-byte chunk is free as long as both sides share it, so a
 // lane's 16 bytes of a row (chunk byte 16 t) serve as they are as the fragments of two MMAs.
-constexpr int LIN8R_WARPS = 8;
 
 __device__ __forceinline__ void mma16832_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                               uint32_t b1) {
@@ -707,19 +706,23 @@ struct Lin8RowsParams {
   int64_t lda, ldw, ldo;
 };
 
-template <int NB>
-__global__ void __launch_bounds__(32 * LIN8R_WARPS) lin8_rows_kernel(Lin8RowsParams r, int* status) {
+template <int NB, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) lin8_rows_kernel(Lin8RowsParams r, int* status) {
   constexpr int U = NB == 1 ? 8 : (NB == 2 ? 6 : 4);  // chunks in flight
-  __shared__ float part[LIN8R_WARPS][16][8 * NB + 1];
+  __shared__ float part[WARPS][16][8 * NB + 1];
   const Lin8Params& p = r.p;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int n0 = blockIdx.x * 16;
+  // the weights on their way into L2 while the kernel ahead finishes (a prefetch takes no value: whoever writes
+  // them is still waited for)
+  if (threadIdx.x < 16 && n0 + static_cast<int>(threadIdx.x) < p.N)
+    prefetch_l2_bulk(r.W + static_cast<int64_t>(n0 + threadIdx.x) * r.ldw, static_cast<uint32_t>(p.K));
   pdl_wait();
   pdl_launch_dependents();
   if (*reinterpret_cast<volatile int*>(op_status(status)) != 0) return;
   const int chunks = (p.K + 63) / 64;
-  const int c1 = static_cast<int>(static_cast<long long>(chunks) * (warp + 1) / LIN8R_WARPS);
+  const int c1 = static_cast<int>(static_cast<long long>(chunks) * (warp + 1) / WARPS);
   float acc[NB][4];
 #pragma unroll
   for (int b = 0; b < NB; ++b) acc[b][0] = acc[b][1] = acc[b][2] = acc[b][3] = 0.f;
@@ -736,7 +739,7 @@ __global__ void __launch_bounds__(32 * LIN8R_WARPS) lin8_rows_kernel(Lin8RowsPar
       mma16832_e4m3(acc[x], a0.z, a1.z, a0.w, a1.w, b[x].z, b[x].w);
     }
   };
-  int c = static_cast<int>(static_cast<long long>(chunks) * warp / LIN8R_WARPS);
+  int c = static_cast<int>(static_cast<long long>(chunks) * warp / WARPS);
   const int whole = min(c1, p.K / 64);  // chunks that K does not cut
   for (; c + U <= whole; c += U) {
     uint4 a0[U], a1[U], b[U][NB];
@@ -770,12 +773,12 @@ __global__ void __launch_bounds__(32 * LIN8R_WARPS) lin8_rows_kernel(Lin8RowsPar
     part[warp][g + 8][x * 8 + t * 2 + 1] = acc[x][3];
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < 16 * 8 * NB; i += 32 * LIN8R_WARPS) {
+  for (int i = threadIdx.x; i < 16 * 8 * NB; i += 32 * WARPS) {
     const int n = i & 15, m = i >> 4;
     if (m >= p.M || n0 + n >= p.N) continue;
     float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < LIN8R_WARPS; ++w) v += part[w][n][m];
+    for (int w = 0; w < WARPS; ++w) v += part[w][n][m];
     const float bias = p.bias != nullptr ? __ldg(p.bias + n0 + n) : 0.f;
     r.out[m * r.ldo + n0 + n] = __float2bfloat16_rn(fmaf(v * __ldg(p.sa + m), __ldg(p.sw + n0 + n), bias));
   }

@@ -255,8 +255,11 @@ cudaError_t launch_lin8_split(const CUtensorMap& a, const CUtensorMap& b, const 
 }
 
 template <int NB>
-cudaError_t launch_lin8_rows(const Lin8RowsParams& r, int* st, cudaStream_t s) {
-  return launch_pdl(lin8_rows_kernel<NB>, dim3((r.p.N + 15) / 16), dim3(32 * LIN8R_WARPS), 0, s, r, st);
+cudaError_t launch_lin8_rows(const Lin8RowsParams& r, int* st, cudaStream_t s, int nsm) {
+  // All CTAs at once: two of 8 warps on an SM or four of 4 (1 x 8192 x 8192: 14.8 us with 8 warps, in two waves)
+  const int ctas = (r.p.N + 15) / 16;
+  if (ctas <= 2 * nsm) return launch_pdl(lin8_rows_kernel<NB, 8>, dim3(ctas), dim3(256), 0, s, r, st);
+  return launch_pdl(lin8_rows_kernel<NB, 4>, dim3(ctas), dim3(128), 0, s, r, st);
 }
 
 // ------------------------------------------------------------------ attention
@@ -396,8 +399,8 @@ vit_status vit_op_linear_fp8(const void* A, int64_t lda, const float* a_scales, 
   if (M <= 16 || (M <= 32 && static_cast<long long>(N) * K <= 1 << 22)) {
     const Lin8RowsParams r{p, static_cast<const uint8_t*>(A), static_cast<const uint8_t*>(W), static_cast<__nv_bfloat16*>(out),
                            M > 1 ? lda : 0, N > 1 ? ldw : 0, M > 1 ? ldo : 0};
-    CK(M <= 8 ? launch_lin8_rows<1>(r, status, s) : M <= 16 ? launch_lin8_rows<2>(r, status, s)
-                                                            : launch_lin8_rows<4>(r, status, s));
+    CK(M <= 8 ? launch_lin8_rows<1>(r, status, s, nsm) : M <= 16 ? launch_lin8_rows<2>(r, status, s, nsm)
+                                                            : launch_lin8_rows<4>(r, status, s, nsm));
     return VIT_OK;
   }
   CUtensorMap ta, tb, to;
