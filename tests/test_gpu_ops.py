@@ -778,3 +778,107 @@ def test_many_rows(rows, D, xt):
     few, _, _ = V.rms_norm(x[:3], w, 1e-6)
     many, _, _ = V.rms_norm(x, w, 1e-6)
     assert ((few.double() - many[:3].double()).abs() <= 2 * u_of(x.dtype) * many[:3].double().abs()).all()
+
+
+# ------------------------------------------------------------------ calls at the edges of what is allowed
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("d", [64, 128])
+def test_attention_broadcast_heads_and_tokens(kernel, d):
+    """Keys and values that are one head's seen as several (a head stride of 0): right, or refused."""
+    V, g = lib(), gen(40)
+    q = randn(g, 70, 4, d, dtype=torch.bfloat16)
+    k1, v1 = randn(g, 70, 1, d, dtype=torch.bfloat16), randn(g, 70, 1, d, dtype=torch.bfloat16)
+    args = by_kernel(kernel, k1, v1, cum([30, 40]), cum([30, 40]))
+    args["k"], args["v"] = args["k"].expand(-1, 2, -1), args["v"].expand(-1, 2, -1)
+    try:
+        out = V.attention_packed(q, **args, causal=True)
+    except V.VitError as e:
+        assert e.status in (V.VIT_E_CUDA, V.VIT_E_SHAPE)
+        return
+    V.op_poll()
+    check_attn(out, q, k1.expand(-1, 2, -1), v1.expand(-1, 2, -1), [0, 30], [0, 30], [30, 40], [30, 40], True, d ** -0.5)
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_attention_offsets_past_32_bits(kernel):
+    """A cache of more than 2^31 values: the last sequence begins behind them."""
+    V, g = lib(), gen(41)
+    hkv, d, room = 8, 128, 2_200_000
+    lens = [70, 50]
+    kv = torch.empty(2, 2 * room, hkv, d, dtype=torch.bfloat16, device="cuda")
+    for i, ln in enumerate(lens):
+        kv[:, i * room:i * room + ln] = randn(g, 2, ln, hkv, d, dtype=torch.bfloat16)
+        kv[:, i * room + ln:i * room + ln + 64] = NAN
+    k, v = kv[0], kv[1]
+    assert k.stride(0) * room > 1 << 31
+    q = randn(g, 2, 16, d, dtype=torch.bfloat16)
+    cu_q, cu_k = cum([1, 1]), cum([room, room])
+    len_k = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    args = dict(k=k, v=v, cu_q=cu_q, cu_k=cu_k, len_k=len_k, max_q=0 if kernel == "tile" else 1)
+    if kernel == "short":
+        args = by_kernel(kernel, k, v, cu_q, cu_k, len_k)
+    out = V.attention_packed(q, **args, causal=True)
+    V.op_poll()
+    check_attn(out, q, k, v, [0, 1], [0, room], [1, 1], lens, True, d ** -0.5)
+
+
+def test_rows_offsets_past_32_bits():
+    """Rows of a matrix of more than 2^31 values, at its end, through the norm, rope and the 8-bit layer."""
+    V, g = lib(), gen(42)
+    rows, D, ld = 3, 256, 1 << 30
+    big = torch.empty(2 * ld + D, dtype=torch.bfloat16, device="cuda")
+    x = torch.as_strided(big, (rows, D), (ld, 1))
+    x.copy_(randn(g, rows, D, dtype=torch.bfloat16))
+    q, s = V.quant_rows(x)
+    check_rows8(q, s, x.double(), "far rows")
+    heads = torch.as_strided(big, (rows, 2, 128), (ld, 128, 1))
+    pos = torch.arange(rows, device="cuda", dtype=torch.int32) + 7
+    f = V.rope_freqs(10000.0, 128)
+    out, _ = V.rope(heads, None, pos, f)
+    check_rope(out, heads, pos, f, "half")
+    del big, x, heads
+    a = torch.empty(2 * ld + D, dtype=torch.uint8, device="cuda").view(E4M3)
+    far = torch.as_strided(a, (rows, D), (ld, 1))
+    far.copy_(q)
+    w, sw = V.quant_rows(randn(g, 64, D))
+    check_linear(V.linear_fp8(far, s, w, sw), q, s, w, sw, None)
+
+
+def test_first_calls_inside_a_capture():
+    """In a fresh process the first call of every operator may be a captured one."""
+    lib()
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch, vision_transformer_encoder_fwd_b200 as V
+bf = torch.bfloat16
+x = torch.randn(40, 1024, device="cuda", dtype=bf)
+w = torch.ones(1024, device="cuda", dtype=bf)
+wf = torch.zeros(256, 1024, device="cuda").to(torch.float8_e4m3fn)
+sw = torch.ones(256, device="cuda")
+q = torch.randn(40, 4, 64, device="cuda", dtype=bf)
+k = torch.randn(4000, 4, 64, device="cuda", dtype=bf)
+cu = torch.tensor([0, 40], dtype=torch.int32, device="cuda")
+ck = torch.tensor([0, 4000], dtype=torch.int32, device="cuda")
+pos = torch.arange(40, device="cuda")
+f = V.rope_freqs(10000.0, 64)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    a, s, _ = V.rms_norm(x, w, fp8=True)
+    y = V.linear_fp8(a, s, wf, sw)
+    y1 = V.linear_fp8(a[:4], s[:4], wf, sw)
+    r, _ = V.rope(q, None, pos, f)
+    o = [V.attention_packed(r, k, k, cu, ck, max_q=m) for m in (0, 1)]
+    o.append(V.attention_packed(r, k[:40], k[:40], cu, cu, max_q=40))
+g.replay()
+torch.cuda.synchronize()
+V.op_poll()
+for i, t in enumerate([y, y1, r] + o):
+    assert torch.isfinite(t.float()).all(), i
+print("fine")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    res = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert res.returncode == 0 and "fine" in res.stdout, res.stderr[-2000:]
