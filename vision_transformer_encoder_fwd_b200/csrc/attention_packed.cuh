@@ -157,6 +157,12 @@ __device__ __noinline__ bool wait_one_slow(uint32_t bar, uint32_t parity, volati
                                            unsigned long long limit) {
   return mbar_wait<32>(static_cast<uint64_t*>(__cvta_shared_to_generic(bar)), parity, abort_flag, gstatus, site, limit);
 }
+// An arrival without a branch around it.
+__device__ __forceinline__ void arrive_if(bool yes, uint32_t bar) {
+  asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 st;\n\tsetp.ne.b32 p, %1, 0;\n\t@p mbarrier.arrive.shared::cta.b64 st, [%0];\n\t}" ::"r"(bar),
+               "r"(yes ? 1 : 0)
+               : "memory");
+}
 __device__ __forceinline__ bool test_bar(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
@@ -427,16 +433,17 @@ __global__ void __launch_bounds__(ATT_THREADS, AttnPackedCfg<HD>::PER_SM)
     const uint32_t t_o = tmem_base + lane_off + Cfg::TM_O;
     // keys this row sees (<= 0: none); rows of nobody go along with the last one
     const int lim = p.causal ? min(st.lk, min(tok, st.lq - 1) + off + 1) : st.lk;
+    const uint32_t s_done0 = smem_u32(s_done), p_full0 = smem_u32(p_full);
     const int whole = __reduce_min_sync(0xffffffffu, max(lim, 0)) / 64;  // blocks that every row of the warp sees whole
     const float c = p.scale_log2;
-    float m = -INFINITY, l = 0.f;
+    float m = -INFINITY, mc = 0.f, l = 0.f;  // mc: m c, 0 for a row that has seen no key
     bool ok = true;
     // Two CTAs of an SM that start together stay in step, both at their exponentials and then both not: the one
     // with the upper half of tensor memory begins 0.4 us later (8 x 4101 tokens, 16 heads of 64: 795 -> 749
     // us; 2 x 8192, 16 of 128: 899 -> 874; 0.2 and 0.7 us were within 2 %)
     if (nblk > 4 && (tmem_base & 0xffffu) != 0) __nanosleep(400);
     for (int n = 0; n < nblk; ++n) {
-      if (!wait_warp(smem_u32(s_done) + (n % DONE) * 8, static_cast<uint32_t>(n / DONE) & 1u, abort_flag, gstatus, DEV_TIMEOUT_ATTP + 7,
+      if (!wait_warp(s_done0 + (n % DONE) * 8, static_cast<uint32_t>(n / DONE) & 1u, abort_flag, gstatus, DEV_TIMEOUT_ATTP + 7,
                      wlim)) {
         ok = false;
         break;
@@ -453,27 +460,29 @@ __global__ void __launch_bounds__(ATT_THREADS, AttnPackedCfg<HD>::PER_SM)
       }
       const float m_new = fmaxf(m, row_max64(s));
       const bool resc = !((m_new - m) * c <= kRescaleLog2) && m_new != -INFINITY;
-      float alpha = 1.f;
-      if (resc) {
-        alpha = to_max(m, m_new, c);
-        m = m_new;
-        l *= alpha;
-      }
-      if (__builtin_expect(n > 0 && __any_sync(0xffffffffu, resc), 0)) {
-        if (!wait_warp(smem_u32(pv_done) + ((n - 1) % DONE) * 8, static_cast<uint32_t>((n - 1) / DONE) & 1u, abort_flag, gstatus,
-                       DEV_TIMEOUT_ATTP + 8, wlim)) {
-          ok = false;
-          break;
+      if (__builtin_expect(__any_sync(0xffffffffu, resc), 0)) {
+        const float alpha = resc ? to_max(m, m_new, c) : 1.f;
+        if (resc) {
+          m = m_new;
+          mc = max_offset(m, c);
         }
-        tc_fence_after();
+        l *= alpha;
+        if (n > 0) {
+          if (!wait_warp(smem_u32(pv_done) + ((n - 1) % DONE) * 8, static_cast<uint32_t>((n - 1) / DONE) & 1u, abort_flag,
+                         gstatus, DEV_TIMEOUT_ATTP + 8, wlim)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
 #pragma unroll 1
-        for (int u = 0; u < Cfg::O_COLS; u += 16) {
-          float o[16];
-          tmem_ld16(t_o + u, o);
-          uint32_t ob[16];
+          for (int u = 0; u < Cfg::O_COLS; u += 16) {
+            float o[16];
+            tmem_ld16(t_o + u, o);
+            uint32_t ob[16];
 #pragma unroll
-          for (int t = 0; t < 16; ++t) ob[t] = __float_as_uint(o[t] * alpha);
-          tmem_st16(t_o + u, ob);
+            for (int t = 0; t < 16; ++t) ob[t] = __float_as_uint(o[t] * alpha);
+            tmem_st16(t_o + u, ob);
+          }
         }
       }
       if (__builtin_expect(n == nblk - 1 && st.lk < nblk * 64, 0)) {
@@ -491,13 +500,12 @@ __global__ void __launch_bounds__(ATT_THREADS, AttnPackedCfg<HD>::PER_SM)
         }
         fence_proxy_async_smem();
       }
-      const float mc = max_offset(m, c);
       __syncwarp();
       l += packed_p64<T, !Cfg::ONES, HD == 64 ? 4 : 8>(s, c, mc, t_b);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[n & 1]);
+      arrive_if(lane == 0, p_full0 + (n & 1) * 8);
     }
     if (ok && nblk > 0) ok = wait_warp(smem_u32(mma_done), 0, abort_flag, gstatus, DEV_TIMEOUT_ATTP + 10, wlim);
     if (ok) {
