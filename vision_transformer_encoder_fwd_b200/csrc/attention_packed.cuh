@@ -9,17 +9,20 @@
 // One CTA per (tile of 128 rows, group of heads), 6 warps.  A row is one query of one head: the heads
 // of a tile share a key head, `pack` of them side by side (row t * pack + g), so that short sequences
 // with grouped heads still fill a tile.
-//   warp 0      TMA: Q once, then K and V blocks of KEYS keys in the order the MMAs use them
+//   warp 0      TMA: Q once, then K and V blocks of 64 keys in the order the MMAs use them
 //   warp 1      TMEM and the MMAs  S = Q K_n^T (both from shared memory), O += P_n V_n
 //   warps 2..5  softmax, one row per thread; P is written over S
-// The keys are taken in blocks of 64 with two S buffers in tensor memory, so that the S of the next block
-// is there when a softmax ends; two CTAs per SM.  The softmax's exponentials (16 a clock and SM on the
-// special-function unit) bound it at width 64, the MMAs with them at width 128; what costs in practice
-// is the time from one block's P to the S two blocks on, most of it the issuing thread's own.  It is
-// chosen by elect.sync, which lets the compiler keep descriptors in uniform registers (four MMAs and
-// a commit take 135 clocks; 365 under an ordinary predicate), commits once per S and once per O (the
-// copies' slots are freed by the same barriers) and has K and V in hand before it waits for P.  The
-// running maximum moves only when it grows by more than 2^8.
+// There are two S buffers in tensor memory, so that the S of the next block is there when a softmax ends, and two
+// CTAs per SM.  The softmax's exponentials (16 a clock and SM on the special-function unit) bound it at
+// width 64, the MMAs with them at width 128; what it costs in practice is the latency of a row's chain: S
+// from tensor memory, maximum, exponentials, P back, O and the next S (about 1400 clocks for 64 keys, half
+// of it hidden by the other CTA).  The MMAs are issued by a thread chosen by elect.sync, which lets the
+// compiler keep descriptors in uniform registers (four MMAs and a commit take 135 clocks; 365 under an
+// ordinary predicate), with one commit for S and one for O (the copies' slots are freed by the same
+// barriers) and K and V in hand before it waits for P.  The running maximum moves only when it grows by
+// more than 2^8.
+// Measured: 8 x 4101 tokens, 16 heads of 64, 734 us (751 TFLOP/s); 2 x 8192, 16 heads of 128, 875 us (1257
+// TFLOP/s); a causal prompt of 8191, 32 heads on 8 of 128, 538 us (1021 TFLOP/s).
 // What a tile reads past its sequence's last key belongs to somebody else or to nobody and may be
 // NaN: scores there are replaced before use, and V's rows there are overwritten with zeros in
 // shared memory, since 0 * NaN would reach every row of O.
@@ -67,18 +70,22 @@ __device__ __forceinline__ void seq_bounds(const AttnPackedParams& p, int i, Seq
   if (p.len_k != nullptr) s.lk = clampi(p.len_k[i], 0, s.lk);
 }
 
-// Finds tile number `want` in the order of the sequences, ceil(lq * mul / bm) tiles each.  One warp; every lane gets the answer.  Each round takes 128 sequences, four
-// per lane, so that up to that many cost one trip to memory.  seq = -1: there is no such tile.
-__device__ __forceinline__ SeqTile find_tile(const AttnPackedParams& p, int want, int bm,
-                                             int mul = 1) {
+// Finds tile number `want` in the order of the sequences, ceil(lq * mul / bm) tiles each.  One warp; every
+// lane gets the answer.  Each round takes 128 sequences, four per lane, with all their bounds, so that up to
+// that many cost one trip to memory.  seq = -1: there is no such tile.
+__device__ __forceinline__ SeqTile find_tile(const AttnPackedParams& p, int want, int bm, int mul = 1) {
   const int lane = threadIdx.x & 31;
-  SeqTile s;
-  s.seq = -1;
+  SeqTile s{0, 0, 0, 0, 0, -1};
   int before = 0;
   for (int base = 0; base < p.n; base += 128) {
-    int c[5];
+    int c[5], k[5], len[4];
 #pragma unroll
-    for (int u = 0; u < 5; ++u) c[u] = clampi(p.cu_q[min(base + lane * 4 + u, p.n)], 0, p.Tq);
+    for (int u = 0; u < 5; ++u) {
+      const int i = min(base + lane * 4 + u, p.n);
+      c[u] = clampi(p.cu_q[i], 0, p.Tq);
+      k[u] = clampi(p.cu_k[i], 0, p.Tk);
+      if (u < 4) len[u] = p.len_k != nullptr ? p.len_k[min(i, p.n - 1)] : 0x7fffffff;
+    }
     int cnt[4], sum = 0;
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
@@ -93,20 +100,27 @@ __device__ __forceinline__ SeqTile find_tile(const AttnPackedParams& p, int want
     }
     const int total = __shfl_sync(0xffffffffu, incl, 31);
     if (want < before + total) {
-      int at = before + incl - sum, seq = -1, tile = 0;
+      int at = before + incl - sum;
+      SeqTile f{0, 0, 0, 0, 0, -1};
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         if (want >= at && want < at + cnt[u]) {
-          seq = base + lane * 4 + u;
-          tile = want - at;
+          f.seq = base + lane * 4 + u;
+          f.tile = want - at;
+          f.q0 = c[u];
+          f.lq = max(0, c[u + 1] - c[u]);
+          f.k0 = k[u];
+          f.lk = clampi(len[u], 0, max(0, k[u + 1] - k[u]));
         }
         at += cnt[u];
       }
-      const unsigned who = __ballot_sync(0xffffffffu, seq >= 0);
-      const int src = __ffs(static_cast<int>(who)) - 1;
-      s.seq = __shfl_sync(0xffffffffu, seq, src);
-      s.tile = __shfl_sync(0xffffffffu, tile, src);
-      seq_bounds(p, s.seq, s);
+      const int src = __ffs(static_cast<int>(__ballot_sync(0xffffffffu, f.seq >= 0))) - 1;
+      s.q0 = __shfl_sync(0xffffffffu, f.q0, src);
+      s.lq = __shfl_sync(0xffffffffu, f.lq, src);
+      s.k0 = __shfl_sync(0xffffffffu, f.k0, src);
+      s.lk = __shfl_sync(0xffffffffu, f.lk, src);
+      s.tile = __shfl_sync(0xffffffffu, f.tile, src);
+      s.seq = __shfl_sync(0xffffffffu, f.seq, src);
       return s;
     }
     before += total;

