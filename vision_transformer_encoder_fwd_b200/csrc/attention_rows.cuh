@@ -43,8 +43,8 @@ struct AttnRowsCfg {
   static_assert(PER_SM * (SMEM_BYTES + 1024) <= 233472, "CTAs per SM");
 };
 
-// Division by a number known at launch (Granlund and Montgomery): n / d for 0 <= n < 2^31 (multiply by ceil(2^(32+l) / d) - 2^32 with
-// l = ceil(log2 d), of which n is the part the multiplier's 33rd bit adds).
+// Division by a number known at launch (Granlund and Montgomery): n / d for 0 <= n < 2^31, by a multiplier of 33
+// bits, ceil(2^(32+l) / d) with l = ceil(log2 d), whose top bit is the n that is added.
 struct FastDiv {
   uint32_t d, mul, shift;
 };

@@ -116,8 +116,13 @@ struct RowsParams {
 // One row per group of `tpr` threads (a power of two, or the whole block); NV vectors of E values
 // per thread, vector v of thread t at element (v * tpr + t) * E.
 // RMODE: 0 no residual, 1 residual of x's type, 2 fp32 residual.
+// Bounds that leave enough rows on an SM: 8191 rows of 4096, us with 2 / 3 / 4 blocks of 512: residual of x's type 49 /
+// 47 / 68, fp32 60 / 65 / 92; rows of 5701 in single values 72 with one block of 1024, 54 with two.
+constexpr int rows_threads(int e, int nv) { return e == 8 && nv < 4 ? 512 : 1024; }
+constexpr int rows_blocks(int e, int nv, int rmode) { return e == 8 && nv < 4 ? (rmode == 1 ? 3 : 2) : nv == 8 ? 2 : 1; }
+
 template <typename TX, int RMODE, bool OUT8, int E, int NV>
-__global__ void __launch_bounds__(E == 8 && NV < 4 ? 512 : 1024, E == 8 && NV < 4 ? (RMODE == 1 ? 3 : 2) : NV == 8 ? 2 : 1) rows_kernel(RowsParams p, int tpr) {
+__global__ void __launch_bounds__(rows_threads(E, NV), rows_blocks(E, NV, RMODE)) rows_kernel(RowsParams p, int tpr) {
   using TR = typename std::conditional<RMODE == 2, float, TX>::type;
   constexpr bool VEC = E > 1;
   __shared__ float2 part[32];
