@@ -107,6 +107,53 @@ def test_rms_norm_strides_in_place_and_stream():
         assert torch.equal(res[:, :4], before_res[:, :4]) and torch.equal(res[:, 204:], before_res[:, 204:])
 
 
+@pytest.mark.parametrize("rt", [None, "same", "fp32"])
+@pytest.mark.parametrize("xt", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("D", [1, 9, 65, 263, 497, 519, 1003, 2055, 4090, 8179, 8199, 16391, 20007, 32767])
+def test_rows_that_begin_anywhere(D, xt, rt):
+    """Rows of any width behind one another and with gaps (NaN, which stays), the operands' strides the same modulo
+    8 elements or not."""
+    V, g = lib(), gen(D)
+    rows, dt = 9, DT[xt]
+    w = (1 + randn(g, D, scale=0.3)).to(dt)
+    x = randn(g, rows, D, dtype=dt, scale=2.0)
+    r = None if rt is None else randn(g, rows, D, dtype=dt if rt == "same" else torch.float32)
+    xd, rd = x.double(), 0 if r is None else r.double()
+    hd = xd + rd
+    rms = torch.sqrt(hd.square().mean(dim=1, keepdim=True) + 1e-5)
+    y = hd / rms * w.double()
+    # the residual's sum in fp32 is off by 2^-24 of its parts, where they cancel too
+    slack = (xd.abs() + (0 if r is None else rd.abs())) * w.double().abs() * 2.0 ** -23 / rms
+
+    def wide(t, gap):
+        big = torch.full((rows, D + gap), NAN, device="cuda").to(t)
+        return big, big[:, :D]
+
+    for e4m3 in (False, True):
+        for gaps in ((0, 0, 0, 0), (3, 11, 3, 19), (3, 3, 4, 5)):
+            xb, xv = wide(dt, gaps[0])
+            xv.copy_(x)
+            ob, ov = wide(E4M3 if e4m3 else dt, gaps[1])
+            rv = hv = hb = None
+            if r is not None:
+                rv = wide(r.dtype, gaps[2])[1]
+                rv.copy_(r)
+                hb, hv = wide(r.dtype, gaps[3])
+            out, scales, h = V.rms_norm(xv, w, 1e-5, residual=rv, residual_out=hv, out=ov, fp8=e4m3)
+            if r is not None:
+                assert torch.equal(h, (x.float() + r.float()).to(r.dtype))
+            if e4m3:
+                want_s = y.abs().amax(dim=1).clamp_min(2.0 ** -100) / 448
+                assert ((scales.double() - want_s).abs() <= NORM32 * want_s + slack.amax(dim=1) / 448).all()
+                s = scales.double()[:, None]
+                assert ((out.double() * s - y).abs() <= y.abs() * (2.0 ** -4 + 4 * NORM32) + 2 * slack + s * 2.0 ** -10).all()
+            else:
+                tiny = 2.0 ** -25 if xt == "fp16" else 0.0  # half of fp16's smallest step
+                assert ((out.double() - y).abs() <= y.abs() * (u_of(dt) + NORM32) * 1.01 + 2 * slack + tiny).all()
+            assert ob[:, D:].float().isnan().all() and (hb is None or hb[:, D:].isnan().all())
+            assert xb[:, D:].isnan().all()
+
+
 @pytest.mark.parametrize("D", [64, 1024, 16384, 7])
 def test_rows_with_nan_infinity_and_zeros(D):
     """A NaN or an infinity reaches its own row only; rows of zeros and of tiny values stay finite."""

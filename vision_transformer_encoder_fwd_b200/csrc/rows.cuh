@@ -116,15 +116,24 @@ struct RowsParams {
 // One row per group of `tpr` threads (a power of two, or the whole block); NV vectors of E values
 // per thread, vector v of thread t at element (v * tpr + t) * E.
 // RMODE: 0 no residual, 1 residual of x's type, 2 fp32 residual.
+// SHIFT: rows that begin anywhere, all operands' at the same place modulo 8 elements (rows of odd width behind one
+// another): the vectors are those that lie whole in the row, the up to 7 values before them and after them go to
+// one thread each.  The weights, which begin elsewhere, come from the L1 cache one by one, and bound it with their
+// instructions (us here and by single values: 8191 rows of 4095 with an fp32 residual to 8 bits 70 and 140, of 4097
+// with a bf16 one 59 and 152, of 4093 without 46 and 77; 4000 of 12285 with a bf16 one 116 and 407).
 // Bounds that leave enough rows on an SM: 8191 rows of 4096, us with 2 / 3 / 4 blocks of 512: residual of x's type 49 /
 // 47 / 68, fp32 60 / 65 / 92; rows of 5701 in single values 72 with one block of 1024, 54 with two.
-constexpr int rows_threads(int e, int nv) { return e == 8 && nv < 4 ? 512 : 1024; }
-constexpr int rows_blocks(int e, int nv, int rmode) { return e == 8 && nv < 4 ? (rmode == 1 ? 3 : 2) : nv == 8 ? 2 : 1; }
+constexpr int rows_threads(int e, int nv, int rmode, bool shift) { return e == 8 && nv < 4 && rmode == 1 && !shift ? 512 : 1024; }
+constexpr int rows_blocks(int e, int nv, int rmode, bool shift) {
+  return rows_threads(e, nv, rmode, shift) == 512 ? 3 : nv == 8 ? 2 : 1;
+}
 
-template <typename TX, int RMODE, bool OUT8, int E, int NV>
-__global__ void __launch_bounds__(rows_threads(E, NV), rows_blocks(E, NV, RMODE)) rows_kernel(RowsParams p, int tpr) {
+template <typename TX, int RMODE, bool OUT8, int E, int NV, bool SHIFT = false>
+__global__ void __launch_bounds__(rows_threads(E, NV, RMODE, SHIFT), rows_blocks(E, NV, RMODE, SHIFT))
+    rows_kernel(RowsParams p, int tpr) {
   using TR = typename std::conditional<RMODE == 2, float, TX>::type;
   constexpr bool VEC = E > 1;
+  static_assert(!SHIFT || E == 8, "vectors of 8 values");
   __shared__ float2 part[32];
   const int grp = threadIdx.x / tpr;
   const int t = threadIdx.x - grp * tpr;
@@ -133,12 +142,25 @@ __global__ void __launch_bounds__(rows_threads(E, NV), rows_blocks(E, NV, RMODE)
   pdl_launch_dependents();
   const bool live = row < p.rows;
   const bool norm = p.w != nullptr;
+  // the vectors' part of the row, and the value beside it that is this thread's (-1: none)
+  const int begin = SHIFT ? min(static_cast<int>(-(row * p.x_ld) & 7), p.D) : 0;
+  const int end = SHIFT ? begin + ((p.D - begin) & ~7) : p.D;
+  int extra = -1;
+  if (SHIFT && live) {
+    if (t < begin) extra = t;
+    if (t >= 8 && end + t - 8 < p.D) extra = end + t - 8;
+  }
   float h[NV][E], g[NV][E];
-  float ss = 0.f, top = 0.f;
+  float ss = 0.f, top = 0.f, he = 0.f, ge = 0.f;
+  if (SHIFT && extra >= 0) {
+    he = to_f32<TX>(static_cast<const TX*>(p.x)[row * p.x_ld + extra]);
+    if (RMODE != 0) he += to_f32<TR>(static_cast<const TR*>(p.r)[row * p.r_ld + extra]);
+    if (norm) ge = p.w_f32 ? static_cast<const float*>(p.w)[extra] : to_f32<TX>(static_cast<const TX*>(p.w)[extra]);
+  }
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
-    const int c = (v * tpr + t) * E;
-    if (live && c < p.D) {
+    const int c = begin + (v * tpr + t) * E;
+    if (live && c < end) {
       load_f32<TX, E, VEC>(static_cast<const TX*>(p.x) + row * p.x_ld + c, h[v]);
       if (RMODE != 0) {
         float r[E];
@@ -148,9 +170,9 @@ __global__ void __launch_bounds__(rows_threads(E, NV), rows_blocks(E, NV, RMODE)
       }
       if (norm) {
         if (p.w_f32)
-          load_f32<float, E, VEC>(static_cast<const float*>(p.w) + c, g[v]);
+          load_f32<float, E, VEC && !SHIFT>(static_cast<const float*>(p.w) + c, g[v]);
         else
-          load_f32<TX, E, VEC>(static_cast<const TX*>(p.w) + c, g[v]);
+          load_f32<TX, E, VEC && !SHIFT>(static_cast<const TX*>(p.w) + c, g[v]);
       }
     } else {
 #pragma unroll
@@ -159,8 +181,8 @@ __global__ void __launch_bounds__(rows_threads(E, NV), rows_blocks(E, NV, RMODE)
   }
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
-    const int c = (v * tpr + t) * E;
-    if (RMODE != 0 && live && c < p.D)
+    const int c = begin + (v * tpr + t) * E;
+    if (RMODE != 0 && live && c < end)
       store_f32<TR, E, VEC>(static_cast<TR*>(p.h) + row * p.h_ld + c, h[v]);
 #pragma unroll
     for (int i = 0; i < E; ++i) {
@@ -168,6 +190,12 @@ __global__ void __launch_bounds__(rows_threads(E, NV), rows_blocks(E, NV, RMODE)
       if (norm) h[v][i] *= g[v][i];
       if (OUT8) top = max_nan(top, fabsf(h[v][i]));
     }
+  }
+  if (SHIFT) {
+    if (RMODE != 0 && extra >= 0) static_cast<TR*>(p.h)[row * p.h_ld + extra] = from_f32<TR>(he);
+    ss = fmaf(he, he, ss);
+    if (norm) he *= ge;
+    if (OUT8) top = max_nan(top, fabsf(he));
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -197,10 +225,16 @@ __global__ void __launch_bounds__(rows_threads(E, NV), rows_blocks(E, NV, RMODE)
     mul = row_factor(top, rstd, amax);
     if (t == 0) p.scales[row] = max_nan(amax, kRowAmaxMin) / kE4m3Max;
   }
+  if (SHIFT && extra >= 0) {
+    if (OUT8)
+      static_cast<uint8_t*>(p.out)[row * p.out_ld + extra] = static_cast<uint8_t>(e4m3x2(he * mul, 0.f));
+    else
+      static_cast<TX*>(p.out)[row * p.out_ld + extra] = from_f32<TX>(he * mul);
+  }
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
-    const int c = (v * tpr + t) * E;
-    if (c >= p.D) continue;
+    const int c = begin + (v * tpr + t) * E;
+    if (c >= end) continue;
 #pragma unroll
     for (int i = 0; i < E; ++i) h[v][i] *= mul;
     if (OUT8) {
