@@ -929,3 +929,45 @@ print("fine")
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     res = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
     assert res.returncode == 0 and "fine" in res.stdout, res.stderr[-2000:]
+
+
+@pytest.mark.parametrize("xt,rt", [("fp32", None), ("bf16", None), ("bf16", "fp32"), ("fp32", "fp32")])
+@pytest.mark.parametrize("rows,D", [(6, 7), (6, 64), (6, 1003), (6, 4096), (6, 16392), (9000, 256), (3001, 4096)])
+def test_rows8_for_a_small_eps(rows, D, xt, rt):
+    """Rows of zeros and of values so small that the factor which takes them to 8 bits is past fp32's range: the
+    definition is finite there.  Widths and numbers of rows of each of the kernel's forms."""
+    V, g = lib(), gen(50)
+    dt = DT[xt]
+    x = randn(g, rows, D, dtype=dt)
+    x[1] = 0
+    x[2] = 0
+    x[2, D // 2] = 3e-19
+    x[3] = (randn(g, D) * 1e-19).to(dt)
+    r = None if rt is None else torch.zeros(rows, D, device="cuda", dtype=DT[rt])
+    for eps in (1e-12, 1e-30):
+        for scale in (1.0, 1e-18):
+            w = (1 + 0.3 * torch.rand(D, generator=g, device="cuda")) * scale
+            out, s, _ = V.rms_norm(x, w, eps, residual=r, fp8=True)
+            xd = x.double()
+            # eps as the call takes it: in fp32
+            y = xd / torch.sqrt(xd.square().mean(dim=1, keepdim=True) + float(torch.tensor(eps))) * w.double()
+            assert (out.float()[1] == 0).all() and s[1] == torch.tensor(2.0 ** -100 / 448)
+            assert torch.isfinite(out.float()).all() and torch.isfinite(s).all()
+            # h w of 1e-19 x 1e-18 is held to 2^-149 of fp32's range, relative to 1e-37 less than 2^-24
+            check_rows8(out, s, y, (eps, scale))
+
+
+@pytest.mark.parametrize("rows,D", [(3, 64), (3, 1003), (3, 4096), (6000, 256)])
+def test_rows8_of_an_infinity(rows, D):
+    """With an infinity in a row the norm's scale is NaN (0 times infinity), and so is all that is divided by it; without
+    the norm the scale is infinity, finite values are 0 and the infinity NaN."""
+    V, g = lib(), gen(51)
+    x = randn(g, rows, D)
+    x[1, D // 3] = -math.inf
+    for t in (torch.float32, torch.bfloat16):
+        out, s, _ = V.rms_norm(x.to(t), torch.ones(D, device="cuda"), 1e-6, fp8=True)
+        assert s[1].isnan() and out.float()[1].isnan().all()
+        assert torch.isfinite(out.float()[[0, 2]]).all() and torch.isfinite(s[[0, 2]]).all()
+        q, s = V.quant_rows(x.to(t))
+        assert torch.isinf(s[1]) and q.float()[1, D // 3].isnan()
+        assert (q.float()[1, torch.arange(D, device="cuda") != D // 3] == 0).all()

@@ -94,9 +94,18 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 
 // What the values v = h w of a row are multiplied by on their way to 8 bits: rstd / s with s = top rstd / 448, so
 // that rstd drops out and only the quotient is rounded.  `amax` is top rstd; below the smallest one the
-// scale is that one's.
-__device__ __forceinline__ float row_factor(float top, float rstd, float amax) {
-  return amax <= kRowAmaxMin ? rstd * (kE4m3Max / kRowAmaxMin) : kE4m3Max / top;
+// scale is that one's.  There, and where 448 / top is past fp32's range, the factor itself need not have a
+// number in fp32 (rstd * 448 / 2^-100 from rstd = 6e5 on, which a row of zeros has for eps = 1e-12): v is brought
+// to y = v rstd first (`first`, 1 elsewhere), whose factor 448 / amax is at most 448 * 2^100.  A NaN as
+// amax, which is the scale's, is every value's.
+__device__ __forceinline__ float row_factor(float top, float rstd, float amax, float& first) {
+  float f = kE4m3Max / top;
+  first = 1.0f;
+  if (amax <= kRowAmaxMin || f == INFINITY) {
+    first = rstd;
+    f = kE4m3Max / max_nan(amax, kRowAmaxMin);
+  }
+  return amax == amax ? f : amax;
 }
 
 struct RowsParams {
@@ -222,7 +231,15 @@ __global__ void __launch_bounds__(rows_threads(E, NV, RMODE, SHIFT), rows_blocks
   float mul = rstd;
   if (OUT8) {
     const float amax = top * rstd;
-    mul = row_factor(top, rstd, amax);
+    float first;
+    mul = row_factor(top, rstd, amax, first);
+    if (first != 1.0f) {
+      he *= first;
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int i = 0; i < E; ++i) h[v][i] *= first;
+    }
     if (t == 0) p.scales[row] = max_nan(amax, kRowAmaxMin) / kE4m3Max;
   }
   if (SHIFT && extra >= 0) {
@@ -341,7 +358,14 @@ __global__ void __launch_bounds__(512) rows_stream_kernel(RowsParams p, int tpr)
     float mul = rstd;
     if (OUT8) {
       const float amax = top * rstd;
-      mul = row_factor(top, rstd, amax);
+      float first;
+      mul = row_factor(top, rstd, amax, first);
+      if (first != 1.0f) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) h[v][i] *= first;
+      }
       if (t == 0) p.scales[row] = max_nan(amax, kRowAmaxMin) / kE4m3Max;
     }
 #pragma unroll
