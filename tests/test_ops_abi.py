@@ -261,3 +261,39 @@ def test_attention_workspace_size():
     assert f(ctypes.byref(attn_args(max_q=1, Tk=4096, head_dim=128)), need) == V.VIT_OK and 0 < need.value <= 10 << 20
     assert f(ctypes.byref(attn_args(max_q=1, head_dim=80)), need) == V.VIT_E_UNSUPPORTED
     assert f(ctypes.byref(attn_args(max_q=1)), None) == V.VIT_E_INVALID_ARG
+
+
+def _copy_of_the_package(to):
+    """The package with its headers and built files (times kept, so that nothing in them is stale)."""
+    import shutil
+    name = os.path.basename(os.path.dirname(V.__file__))
+    ops._build.build()
+    for d in (name, "include"):
+        shutil.copytree(os.path.join(ROOT, d), to / d, ignore=shutil.ignore_patterns("__pycache__"))
+    return to / name
+
+
+def _python(code, cwd, **env):
+    import sys
+    return subprocess.run([sys.executable, "-c", code], cwd=cwd, capture_output=True, text=True, timeout=600,
+                          env={**os.environ, "PYTHONPATH": str(cwd), **env})
+
+
+def test_binding_built_late_uses_the_loaded_library(tmp_path):
+    """A process that has loaded the library and then builds the missing binding has one copy of the library; one
+    whose library had to be rebuilt for it is told so."""
+    pkg = _copy_of_the_package(tmp_path)
+    code = f"""
+import os, {pkg.name} as V
+V.load_library()
+os.remove(V.ops._build.BIND_PATH)
+CHANGE
+V.ops._load()
+files = {{l.split()[4] for l in open("/proc/self/maps") if "libvit_b200.so" in l}}
+assert len(files) == 1, files
+print("one library")
+"""
+    res = _python(code.replace("CHANGE", ""), tmp_path)
+    assert "one library" in res.stdout, res.stderr[-2000:]
+    res = _python(code.replace("CHANGE", "os.utime(V.ops._build._sources()[0][1])"), tmp_path)
+    assert res.returncode != 0 and "start the process again" in res.stderr, res.stderr[-2000:]

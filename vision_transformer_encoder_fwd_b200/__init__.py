@@ -113,6 +113,11 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     return lib
 
 
+def library_loaded() -> bool:
+    """Whether this process has loaded the library."""
+    return _lib is not None
+
+
 def _check(fn: str, st: int) -> None:
     if st != VIT_OK:
         lib = load_library()

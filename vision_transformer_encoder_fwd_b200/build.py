@@ -14,7 +14,6 @@ headers that calls the library next to it.
 from __future__ import annotations
 
 import argparse
-import glob
 import os
 import shutil
 import subprocess
@@ -38,9 +37,8 @@ def _nvcc() -> str:
 
 
 def _sources():
-    deps = sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cuh")) +
-                  glob.glob(os.path.join(CSRC, "*.cpp")) + glob.glob(os.path.join(ROOT, "include", "*.h")))
-    return [os.path.join(CSRC, "vit_api.cu"), os.path.join(CSRC, "ops_api.cu")], deps
+    """The library's translation units with their objects."""
+    return [(os.path.join(CSRC, n + ".cu"), os.path.join(OBJ_DIR, n + ".o")) for n in ("vit_api", "ops_api")]
 
 
 def _object_current(obj: str) -> bool:
@@ -54,11 +52,18 @@ def _object_current(obj: str) -> bool:
         return False
 
 
-def up_to_date() -> bool:
-    if not (os.path.exists(LIB_PATH) and os.path.exists(BIND_PATH)):
+def _linked(out: str, objs) -> bool:
+    """Whether `out` is there and no older than the objects it is linked from."""
+    try:
+        return all(os.path.getmtime(o) <= os.path.getmtime(out) for o in objs)
+    except OSError:
         return False
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(BIND_PATH))
-    return all(os.path.getmtime(d) <= t for d in _sources()[1])
+
+
+def up_to_date() -> bool:
+    objs = [obj for _, obj in _sources()]
+    bind = os.path.join(OBJ_DIR, "ops_bind.o")
+    return all(_object_current(o) for o in [*objs, bind]) and _linked(LIB_PATH, objs) and _linked(BIND_PATH, [bind])
 
 
 def _bind_commands(obj: str):
@@ -84,14 +89,12 @@ def _bind_commands(obj: str):
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     if not force and up_to_date():
         return LIB_PATH
-    srcs, _ = _sources()
     os.makedirs(OBJ_DIR, exist_ok=True)
     flags = [*ARCH_FLAGS, "-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC,-O2"]
     if verbose_ptxas:
         flags = ["-Xptxas", "-v", *flags]
     objs, running = [], []
-    for src in srcs:
-        obj = os.path.join(OBJ_DIR, os.path.basename(src)[:-3] + ".o")
+    for src, obj in _sources():
         objs.append(obj)
         if force or verbose_ptxas or not _object_current(obj):
             cmd = [_nvcc(), *flags, "-MMD", "-MF", obj + ".d", "-c", "-o", obj, src]
@@ -101,8 +104,10 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     if force or not _object_current(bind):
         running.append(subprocess.Popen(bind_compile, cwd=ROOT, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True))
     said = [(p.communicate()[0], p.returncode) for p in running]
+    # a library that is current stays the file it is: a process may have it loaded
+    relink = force or not _linked(LIB_PATH, objs)
     tmp = LIB_PATH + ".tmp"
-    if all(rc == 0 for _, rc in said):
+    if relink and all(rc == 0 for _, rc in said):
         p = subprocess.run([_nvcc(), *ARCH_FLAGS, "-shared", "-cudart", "static", "-o", tmp, *objs], cwd=ROOT,
                            capture_output=True, text=True)
         said.append((p.stdout + p.stderr, p.returncode))
@@ -111,7 +116,8 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
         sys.stderr.write("".join(text for text, _ in said))
     if bad:
         raise RuntimeError(f"a compiler failed with exit code {bad[0]}")
-    os.replace(tmp, LIB_PATH)
+    if relink:
+        os.replace(tmp, LIB_PATH)
     p = subprocess.run(bind_link, cwd=ROOT, capture_output=True, text=True)
     if p.returncode != 0:
         sys.stderr.write(p.stdout + p.stderr)

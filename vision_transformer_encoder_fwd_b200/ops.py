@@ -13,7 +13,7 @@ import ctypes
 import os
 from typing import Optional
 
-from . import VIT_E_SHAPE, VIT_E_UNSUPPORTED, VitError, _build, _check, load_library
+from . import VIT_E_SHAPE, VIT_E_UNSUPPORTED, VitError, _build, _check, library_loaded, load_library
 
 ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
 ROPE_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "parts": 3}
@@ -73,12 +73,19 @@ def _fn(name):
 
 
 def _load():
-    """The extension module (built first if it is absent and the compilers are available)."""
+    """The extension module (built first if it is absent and the compilers are available).
+
+    It is linked against the library by name, so it has to find the very file that this process has loaded or
+    will load: with two copies of the library in a process, polls would read the status word of the other one."""
     global _bind
     import torch  # noqa: F401  (its libraries have to be loaded before the module that uses them)
-    load_library()
     if not os.path.exists(_build.BIND_PATH):
+        before = os.stat(_build.LIB_PATH) if library_loaded() else None
         _build.build()
+        if before is not None and not os.path.samestat(before, os.stat(_build.LIB_PATH)):
+            raise ImportError("libvit_b200.so was rebuilt, with the operators' binding, after this process had loaded it: "
+                              "start the process again")
+    load_library()
     from . import _vit_ops
     _vit_ops.set_error(VitError)
     _bind = _vit_ops
