@@ -297,3 +297,24 @@ print("one library")
     assert "one library" in res.stdout, res.stderr[-2000:]
     res = _python(code.replace("CHANGE", "os.utime(V.ops._build._sources()[0][1])"), tmp_path)
     assert res.returncode != 0 and "start the process again" in res.stderr, res.stderr[-2000:]
+
+
+def test_binding_follows_torch(monkeypatch):
+    """A binding of another torch (or of other flags) is stale for the build, and refused when it is loaded."""
+    ops._build.build()
+    assert ops._build.up_to_date()
+    if ops._bind is None:
+        ops._load()
+    loaded = ops._bind
+    with monkeypatch.context() as m:
+        m.setenv("CXX", "another-compiler")
+        assert not ops._build.up_to_date()
+    with monkeypatch.context() as m:
+        m.setattr(ops._build, "ARCH_FLAGS", [*ops._build.ARCH_FLAGS, "-G"])
+        assert not ops._build.up_to_date()
+    with monkeypatch.context() as m:
+        m.setattr(torch, "__version__", "1.0.0")
+        assert not ops._build.up_to_date()
+        with pytest.raises(ImportError, match="built against torch"):
+            ops._load()
+    assert ops._build.up_to_date() and ops._load() is loaded

@@ -6,7 +6,7 @@ The library is two translation units (csrc/vit_api.cu, the encoder, and csrc/ops
 operators; each includes its kernel headers), compiled side by side.  It links the CUDA runtime
 statically and resolves the driver's tensor-map encoder at run time, so it needs no libcuda at
 link time and cross-compiles on a machine without a GPU.  The objects stay in _build/ and are
-kept while none of the files that went into them has changed.
+kept while neither the files that went into them nor the compiler's flags have changed.
 
 csrc/ops_bind.cpp becomes _vit_ops.so, the operators' binding: an extension module against torch's
 headers that calls the library next to it.
@@ -26,6 +26,7 @@ LIB_NAME = "libvit_b200.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 BIND_PATH = os.path.join(PKG_DIR, "_vit_ops.so")
 OBJ_DIR = os.path.join(PKG_DIR, "_build")
+BIND_OBJ = os.path.join(OBJ_DIR, "ops_bind.o")
 ARCH_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -41,9 +42,13 @@ def _sources():
     return [(os.path.join(CSRC, n + ".cu"), os.path.join(OBJ_DIR, n + ".o")) for n in ("vit_api", "ops_api")]
 
 
-def _object_current(obj: str) -> bool:
-    """Whether `obj` is newer than every file its dependency list (written by the compiler) names."""
+def _object_current(obj: str, how) -> bool:
+    """Whether `obj` was compiled with the flags `how` and is newer than every file of this tree that
+    its dependency list (written by the compiler) names."""
     try:
+        with open(obj + ".flags") as f:
+            if f.read() != " ".join(how):
+                return False
         with open(obj + ".d") as f:
             names = f.read().replace("\\\n", " ").split(":", 1)[1].split()
         t = os.path.getmtime(obj)
@@ -62,48 +67,62 @@ def _linked(out: str, objs) -> bool:
 
 def up_to_date() -> bool:
     objs = [obj for _, obj in _sources()]
-    bind = os.path.join(OBJ_DIR, "ops_bind.o")
-    return all(_object_current(o) for o in [*objs, bind]) and _linked(LIB_PATH, objs) and _linked(BIND_PATH, [bind])
+    return (all(_object_current(o, _lib_flags()) for o in objs) and _linked(LIB_PATH, objs) and
+            _object_current(BIND_OBJ, _bind_flags()) and _linked(BIND_PATH, [BIND_OBJ]))
 
 
-def _bind_commands(obj: str):
-    """Compile and link commands of the operators' binding."""
+def _lib_flags():
+    return [*ARCH_FLAGS, "-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC,-O2"]
+
+
+def _bind_flags():
+    """Compiler and flags of the operators' binding.  They name what it is compiled against, whose headers its
+    dependency list leaves out: torch and its version, its C++ ABI, Python."""
     import sysconfig
 
     import torch
-    base = os.path.dirname(torch.__file__)
-    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    base = os.path.join(os.path.dirname(torch.__file__), "include")
     inc = ["-I" + sysconfig.get_paths()["include"]]
-    for d in (os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
-              os.path.join(cuda, "include")):
+    for d in (base, os.path.join(base, "torch", "csrc", "api", "include")):
         inc += ["-isystem", d]
-    libs = os.path.join(base, "lib")
-    cc = os.environ.get("CXX") or "g++"
-    abi = f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"
-    return ([cc, "-O2", "-fPIC", "-std=c++20", abi, *inc, "-MMD", "-MF", obj + ".d", "-c", "-o", obj,
-             os.path.join(CSRC, "ops_bind.cpp")],
-            [cc, "-shared", "-o", BIND_PATH + ".tmp", obj, "-L" + libs, "-L" + PKG_DIR, "-ltorch_python", "-ltorch_cpu",
-             "-ltorch", "-lc10", "-lc10_cuda", "-l:" + LIB_NAME, "-Wl,-rpath,$ORIGIN"])
+    return [os.environ.get("CXX") or "g++", "-O2", "-fPIC", "-std=c++20",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DVIT_TORCH_VERSION="{torch.__version__}"',
+            *inc]
+
+
+def _bind_link():
+    import torch
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    return [os.environ.get("CXX") or "g++", "-shared", "-o", BIND_PATH + ".tmp", BIND_OBJ, "-L" + libs, "-L" + PKG_DIR,
+            "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_cuda", "-l:" + LIB_NAME, "-Wl,-rpath,$ORIGIN"]
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     if not force and up_to_date():
         return LIB_PATH
     os.makedirs(OBJ_DIR, exist_ok=True)
-    flags = [*ARCH_FLAGS, "-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC,-O2"]
-    if verbose_ptxas:
-        flags = ["-Xptxas", "-v", *flags]
     objs, running = [], []
+
+    def compile_object(src, obj, how, before=(), extra=()):
+        if os.path.exists(obj + ".flags"):
+            os.remove(obj + ".flags")  # written again once the object is there
+        cmd = [*before, *how, *extra, "-MMD", "-MF", obj + ".d", "-c", "-o", obj, src]
+        p = subprocess.Popen(cmd, cwd=ROOT, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+        running.append((p, obj, how))
+
     for src, obj in _sources():
         objs.append(obj)
-        if force or verbose_ptxas or not _object_current(obj):
-            cmd = [_nvcc(), *flags, "-MMD", "-MF", obj + ".d", "-c", "-o", obj, src]
-            running.append(subprocess.Popen(cmd, cwd=ROOT, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True))
-    bind = os.path.join(OBJ_DIR, "ops_bind.o")
-    bind_compile, bind_link = _bind_commands(bind)
-    if force or not _object_current(bind):
-        running.append(subprocess.Popen(bind_compile, cwd=ROOT, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True))
-    said = [(p.communicate()[0], p.returncode) for p in running]
+        if force or verbose_ptxas or not _object_current(obj, _lib_flags()):
+            compile_object(src, obj, _lib_flags(), [_nvcc()], ["-Xptxas", "-v"] if verbose_ptxas else [])
+    if force or not _object_current(BIND_OBJ, _bind_flags()):
+        compile_object(os.path.join(CSRC, "ops_bind.cpp"), BIND_OBJ, _bind_flags(),
+                       extra=["-isystem", os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")])
+    said = []
+    for p, obj, how in running:
+        said.append((p.communicate()[0], p.returncode))
+        if p.returncode == 0:
+            with open(obj + ".flags", "w") as f:
+                f.write(" ".join(how))
     # a library that is current stays the file it is: a process may have it loaded
     relink = force or not _linked(LIB_PATH, objs)
     tmp = LIB_PATH + ".tmp"
@@ -118,7 +137,7 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
         raise RuntimeError(f"a compiler failed with exit code {bad[0]}")
     if relink:
         os.replace(tmp, LIB_PATH)
-    p = subprocess.run(bind_link, cwd=ROOT, capture_output=True, text=True)
+    p = subprocess.run(_bind_link(), cwd=ROOT, capture_output=True, text=True)
     if p.returncode != 0:
         sys.stderr.write(p.stdout + p.stderr)
         raise RuntimeError(f"linking the operators' binding failed with exit code {p.returncode}")

@@ -400,4 +400,8 @@ PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_vit_ops", nullptr, -1, g_method
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__vit_ops() { return PyModule_Create(&g_module); }
+PyMODINIT_FUNC PyInit__vit_ops() {
+  PyObject* m = PyModule_Create(&g_module);
+  if (m != nullptr && PyModule_AddStringConstant(m, "torch_version", VIT_TORCH_VERSION) < 0) Py_CLEAR(m);
+  return m;
+}

@@ -78,7 +78,7 @@ def _load():
     It is linked against the library by name, so it has to find the very file that this process has loaded or
     will load: with two copies of the library in a process, polls would read the status word of the other one."""
     global _bind
-    import torch  # noqa: F401  (its libraries have to be loaded before the module that uses them)
+    import torch  # its libraries have to be loaded before the module that uses them
     if not os.path.exists(_build.BIND_PATH):
         before = os.stat(_build.LIB_PATH) if library_loaded() else None
         _build.build()
@@ -87,6 +87,9 @@ def _load():
                               "start the process again")
     load_library()
     from . import _vit_ops
+    if _vit_ops.torch_version != torch.__version__:  # it reads tensors by the layout of the headers it was compiled with
+        raise ImportError(f"the operators' binding was built against torch {_vit_ops.torch_version}, this is "
+                          f"{torch.__version__}: run python {_build.__file__}")
     _vit_ops.set_error(VitError)
     _bind = _vit_ops
     return _bind
