@@ -318,3 +318,27 @@ def test_binding_follows_torch(monkeypatch):
         with pytest.raises(ImportError, match="built against torch"):
             ops._load()
     assert ops._build.up_to_date() and ops._load() is loaded
+
+
+def test_library_builds_without_torch_and_without_a_host_compiler_for_the_binding(tmp_path):
+    """nvcc alone is enough for the C ABI."""
+    pkg = _copy_of_the_package(tmp_path)
+    (pkg / V.ops._build.LIB_NAME).unlink()
+    (pkg / "_vit_ops.so").unlink()
+    code = f"""
+import ctypes, os, runpy, sys
+sys.modules["torch"] = None  # importing it raises ImportError
+build = runpy.run_path(os.path.join({pkg.name!r}, "build.py"))
+assert not build["up_to_date"]()
+lib = ctypes.CDLL(build["build"]())
+assert lib.vit_op_quant_rows and not os.path.exists(build["BIND_PATH"]) and build["up_to_date"]()
+print("C ABI")
+"""
+    res = _python(code, tmp_path)
+    assert "C ABI" in res.stdout, res.stderr[-2000:]
+    (pkg / V.ops._build.LIB_NAME).unlink()
+    for cxx in ("false", "no-such-compiler"):
+        code = f"import runpy; print(runpy.run_path('{pkg.name}/build.py')['build']())"
+        res = _python(code, tmp_path, CXX=cxx)
+        assert res.returncode != 0 and "RuntimeError" in res.stderr, res.stderr[-2000:]
+        assert (pkg / V.ops._build.LIB_NAME).exists() and not (pkg / "_vit_ops.so").exists()

@@ -9,7 +9,8 @@ link time and cross-compiles on a machine without a GPU.  The objects stay in _b
 kept while neither the files that went into them nor the compiler's flags have changed.
 
 csrc/ops_bind.cpp becomes _vit_ops.so, the operators' binding: an extension module against torch's
-headers that calls the library next to it.
+headers that calls the library next to it.  It takes a C++20 compiler and torch; the library needs neither, and
+is there without them (for users of the C ABI alone: without torch the binding is left out).
 """
 from __future__ import annotations
 
@@ -67,8 +68,17 @@ def _linked(out: str, objs) -> bool:
 
 def up_to_date() -> bool:
     objs = [obj for _, obj in _sources()]
-    return (all(_object_current(o, _lib_flags()) for o in objs) and _linked(LIB_PATH, objs) and
-            _object_current(BIND_OBJ, _bind_flags()) and _linked(BIND_PATH, [BIND_OBJ]))
+    if not (all(_object_current(o, _lib_flags()) for o in objs) and _linked(LIB_PATH, objs)):
+        return False
+    return not _have_torch() or (_object_current(BIND_OBJ, _bind_flags()) and _linked(BIND_PATH, [BIND_OBJ]))
+
+
+def _have_torch() -> bool:
+    try:
+        import torch  # noqa: F401
+    except ImportError:
+        return False
+    return True
 
 
 def _lib_flags():
@@ -101,48 +111,62 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     if not force and up_to_date():
         return LIB_PATH
     os.makedirs(OBJ_DIR, exist_ok=True)
-    objs, running = [], []
+    running = {}
 
     def compile_object(src, obj, how, before=(), extra=()):
         if os.path.exists(obj + ".flags"):
             os.remove(obj + ".flags")  # written again once the object is there
         cmd = [*before, *how, *extra, "-MMD", "-MF", obj + ".d", "-c", "-o", obj, src]
-        p = subprocess.Popen(cmd, cwd=ROOT, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
-        running.append((p, obj, how))
+        running[obj] = (_start(cmd), how)
 
-    for src, obj in _sources():
-        objs.append(obj)
-        if force or verbose_ptxas or not _object_current(obj, _lib_flags()):
-            compile_object(src, obj, _lib_flags(), [_nvcc()], ["-Xptxas", "-v"] if verbose_ptxas else [])
-    if force or not _object_current(BIND_OBJ, _bind_flags()):
-        compile_object(os.path.join(CSRC, "ops_bind.cpp"), BIND_OBJ, _bind_flags(),
-                       extra=["-isystem", os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")])
-    said = []
-    for p, obj, how in running:
-        said.append((p.communicate()[0], p.returncode))
-        if p.returncode == 0:
+    def finish(obj):
+        p, how = running.pop(obj, (None, None))
+        if p is not None:
+            _end(p, verbose_ptxas)
             with open(obj + ".flags", "w") as f:
                 f.write(" ".join(how))
-    # a library that is current stays the file it is: a process may have it loaded
-    relink = force or not _linked(LIB_PATH, objs)
-    tmp = LIB_PATH + ".tmp"
-    if relink and all(rc == 0 for _, rc in said):
-        p = subprocess.run([_nvcc(), *ARCH_FLAGS, "-shared", "-cudart", "static", "-o", tmp, *objs], cwd=ROOT,
-                           capture_output=True, text=True)
-        said.append((p.stdout + p.stderr, p.returncode))
-    bad = [rc for _, rc in said if rc != 0]
-    if bad or verbose_ptxas:
-        sys.stderr.write("".join(text for text, _ in said))
-    if bad:
-        raise RuntimeError(f"a compiler failed with exit code {bad[0]}")
-    if relink:
-        os.replace(tmp, LIB_PATH)
-    p = subprocess.run(_bind_link(), cwd=ROOT, capture_output=True, text=True)
-    if p.returncode != 0:
-        sys.stderr.write(p.stdout + p.stderr)
-        raise RuntimeError(f"linking the operators' binding failed with exit code {p.returncode}")
-    os.replace(BIND_PATH + ".tmp", BIND_PATH)
+
+    for src, obj in _sources():
+        if force or verbose_ptxas or not _object_current(obj, _lib_flags()):
+            compile_object(src, obj, _lib_flags(), [_nvcc()], ["-Xptxas", "-v"] if verbose_ptxas else [])
+    bind = _have_torch()
+    try:
+        failed = None
+        if bind and (force or not _object_current(BIND_OBJ, _bind_flags())):
+            try:
+                compile_object(os.path.join(CSRC, "ops_bind.cpp"), BIND_OBJ, _bind_flags(),
+                               extra=["-isystem", os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")])
+            except OSError as e:  # no such compiler: the library first
+                failed = e
+        objs = [obj for _, obj in _sources()]
+        for obj in objs:
+            finish(obj)
+        # a library that is current stays the file it is: a process may have it loaded
+        if force or not _linked(LIB_PATH, objs):
+            _end(_start([_nvcc(), *ARCH_FLAGS, "-shared", "-cudart", "static", "-o", LIB_PATH + ".tmp", *objs]))
+            os.replace(LIB_PATH + ".tmp", LIB_PATH)
+        if failed is not None:
+            raise RuntimeError(f"the operators' binding was not built: {failed}") from failed
+        if bind:
+            finish(BIND_OBJ)
+            _end(_start(_bind_link()))
+            os.replace(BIND_PATH + ".tmp", BIND_PATH)
+    finally:
+        for p, _ in running.values():
+            p.communicate()
     return LIB_PATH
+
+
+def _start(cmd):
+    return subprocess.Popen(cmd, cwd=ROOT, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+
+
+def _end(p, show: bool = False) -> None:
+    said = p.communicate()[0]
+    if show or p.returncode != 0:
+        sys.stderr.write(said)
+    if p.returncode != 0:
+        raise RuntimeError(f"{os.path.basename(p.args[0])} failed with exit code {p.returncode}")
 
 
 def main(argv=None):
