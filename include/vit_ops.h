@@ -12,9 +12,11 @@
  * (no rows, no tokens) it returns VIT_OK and enqueues nothing.
  *   - Strides are in elements; the last dimension is contiguous.
  *   - `status`: device int32, zero at the start, that a kernel sets when one of its pipeline waits
- *     gives up and that later kernels on the same word check on entry (they return without work
- *     while it is set); NULL selects a word of the library per device, read and cleared by
- *     vit_op_poll.  `wait_ns`: limit of the waits in nanoseconds, 0 for the default 2 s.
+ *     gives up (what that call was to write is then undefined) and that later kernels on the same word check on
+ *     entry: they return without work while it is set.  NULL selects a word of the library per device,
+ *     which all such calls share: it stops nobody, vit_op_poll reads and clears it, and a caller who has to know
+ *     about its own calls beside others' gives a word of its own.  `wait_ns`: limit of the waits in
+ *     nanoseconds, 0 for the default 2 s.
  */
 #ifndef VIT_B200_OPS_H
 #define VIT_B200_OPS_H

@@ -971,3 +971,27 @@ def test_rows8_of_an_infinity(rows, D):
         q, s = V.quant_rows(x.to(t))
         assert torch.isinf(s[1]) and q.float()[1, D // 3].isnan()
         assert (q.float()[1, torch.arange(D, device="cuda") != D // 3] == 0).all()
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_a_wait_that_ran_out_leaves_other_calls_alone(kernel):
+    """Without a status word of their own, calls after one whose wait ran out do their work; the poll still tells."""
+    V, g = lib(), gen(52)
+    n = 500
+    q, k, v = (randn(g, n, 2, 128, dtype=torch.bfloat16) for _ in range(3))
+    cu = cum([n])
+    V.attention_packed(q, k, v, cu, cu, wait_ns=200)
+    out = torch.full_like(q, 0.5)
+    V.attention_packed(q, **by_kernel(kernel, k, v, cu, cu), out=out)
+    lin = []
+    for M in (5, 200, 2600):
+        a, sa, w, sw, b = make_linear(M, 1024, 2048, 9, True)
+        lin.append((V.linear_fp8(a, sa, w, sw, bias=b, out=torch.full((M, 1024), 7.0, device="cuda", dtype=torch.bfloat16)),
+                    a, sa, w, sw, b))
+    with pytest.raises(V.VitError) as e:
+        V.op_poll()
+    assert e.value.status == V.VIT_E_DEVICE_TIMEOUT
+    V.op_poll()
+    check_attn(out, q, k, v, [0], [0], [n], [n], False, 128 ** -0.5)
+    for r in lin:
+        check_linear(*r)

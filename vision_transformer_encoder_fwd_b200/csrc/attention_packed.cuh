@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(ATT_THREADS, AttnPackedCfg<HD>::PER_SM)
     tmem_relinquish();
   }
   pdl_wait();
-  if (threadIdx.x == 0) *abort_flag = (*reinterpret_cast<volatile int*>(gstatus) != 0) ? 1 : 0;
+  if (threadIdx.x == 0) *abort_flag = op_stopped(status) ? 1 : 0;
   if (warp == 2) {
     const SeqTile f = find_tile(p, static_cast<int>(blockIdx.x), p.tokens);
     if (lane == 0) *s_tile = f;

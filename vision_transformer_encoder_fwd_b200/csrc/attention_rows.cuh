@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(ATTR_THREADS, AttnRowsCfg<HD>::PER_SM)
     tma_prefetch_desc(&tmV);
   }
   pdl_wait();
-  if (threadIdx.x == 0) *abort_flag = (*reinterpret_cast<volatile int*>(gstatus) != 0) ? 1 : 0;
+  if (threadIdx.x == 0) *abort_flag = op_stopped(status) ? 1 : 0;
   long long u = 0, u_end = 0, base = 0, per = 0;
   int seq = 0;
   if (warp == 4) {
@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(32 * ATTJ_WARPS) attn_join_kernel(const __grid
   pdl_wait();
   pdl_launch_dependents();
   __syncthreads();
-  if (s_seq >= p.n || *reinterpret_cast<volatile int*>(op_status(status)) != 0) return;
+  if (s_seq >= p.n || op_stopped(status)) return;
   const long long at = s_at[0], base = s_at[1], per = s_at[2];
   SeqTile s;
   long long nt;

@@ -38,7 +38,7 @@ __global__ void __launch_bounds__(32 * ATTS_WARPS, HD == 64 ? 4 : 2)
   const int group = static_cast<int>(pr.group.d);
   pdl_wait();
   pdl_launch_dependents();
-  if (*reinterpret_cast<volatile int*>(op_status(status)) != 0) return;
+  if (op_stopped(status)) return;
   const SeqTile st = find_tile(p, static_cast<int>(blockIdx.x) * ATTS_WARPS + static_cast<int>(threadIdx.x >> 5), 16, group);
   if (st.seq < 0) return;
   const int rows = st.lq * group;

@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(LIN8_THREADS, 1)
   }
   // everything above touches only this CTA's shared and tensor memory; global memory from here on
   pdl_wait();
-  if (threadIdx.x == 0) *abort_flag = (*reinterpret_cast<volatile int*>(gstatus) != 0) ? 1 : 0;
+  if (threadIdx.x == 0) *abort_flag = op_stopped(status) ? 1 : 0;
   pdl_launch_dependents();
   tc_fence_before();
   __syncthreads();
@@ -356,7 +356,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LIN8_THREADS, 1)
   }
   // everything above touches only this cluster's shared and tensor memory; global memory from here on
   pdl_wait();
-  if (threadIdx.x == 0) *abort_flag = (*reinterpret_cast<volatile int*>(gstatus) != 0) ? 1 : 0;
+  if (threadIdx.x == 0) *abort_flag = op_stopped(status) ? 1 : 0;
   pdl_launch_dependents();
   tc_fence_before();
   cluster_sync_all();
@@ -541,7 +541,7 @@ __global__ void __launch_bounds__(LIN8_THREADS, 1)
     tmem_relinquish();
   }
   pdl_wait();
-  if (threadIdx.x == 0) *abort_flag = (*reinterpret_cast<volatile int*>(gstatus) != 0) ? 1 : 0;
+  if (threadIdx.x == 0) *abort_flag = op_stopped(status) ? 1 : 0;
   pdl_launch_dependents();
   tc_fence_before();
   __syncthreads();
@@ -721,7 +721,7 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) lin8_rows_kernel(Lin8R
     prefetch_l2_bulk(r.W + static_cast<int64_t>(n0 + threadIdx.x) * r.ldw, static_cast<uint32_t>(p.K));
   pdl_wait();
   pdl_launch_dependents();
-  if (*reinterpret_cast<volatile int*>(op_status(status)) != 0) return;
+  if (op_stopped(status)) return;
   const int chunks = (p.K + 63) / 64;
   const int c1 = static_cast<int>(static_cast<long long>(chunks) * (warp + 1) / WARPS);
   float acc[NB][4];
