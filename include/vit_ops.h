@@ -44,9 +44,11 @@ typedef enum vit_dtype {
  *   x: [rows, D], leading dimension x_ld, bf16 / fp16 / fp32.
  *   residual, residual_out: both or neither; same shape, x's type or fp32; may be the same memory.
  *   weight: [D], x's type or fp32.       out: [rows, D].      scales: fp32 [rows], E4M3 only.
- * out may be x.  1 <= D <= 32768; pointers aligned to their element type.  Rows on 16-byte aligned
- * pointers (an 8-bit out: 8) take 16-byte accesses if their leading dimensions are the same modulo 8,
- * fastest where those and D are multiples of 8. */
+ * out may be x, residual_out residual, with the same bytes from row to row (E4M3 on a 16-bit x: out_ld = 2 x_ld);
+ * otherwise nothing that is written overlaps what the call reads or writes.
+ * 1 <= D <= 32768; pointers aligned to their element type.  Rows on 16-byte aligned pointers (an 8-bit out: 8)
+ * take 16-byte accesses if their leading dimensions are the same modulo 8, fastest where those and D are
+ * multiples of 8. */
 vit_status vit_op_rms_norm(const void *x, vit_dtype x_type, int64_t x_ld, const void *residual, int64_t residual_ld,
                            void *residual_out, int64_t residual_out_ld, vit_dtype residual_type, const void *weight,
                            vit_dtype weight_type, float eps, int64_t rows, int32_t D, void *out, vit_dtype out_type,

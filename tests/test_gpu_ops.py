@@ -995,3 +995,26 @@ def test_a_wait_that_ran_out_leaves_other_calls_alone(kernel):
     check_attn(out, q, k, v, [0], [0], [n], [n], False, 128 ** -0.5)
     for r in lin:
         check_linear(*r)
+
+
+@pytest.mark.parametrize("xt", ["bf16", "fp32"])
+@pytest.mark.parametrize("rows,D", [(1, 64), (7, 64), (9, 1003), (8, 4096), (6000, 256), (3001, 4096), (2000, 1023)])
+def test_rows_on_their_inputs(rows, D, xt):
+    """out on x (of x's type, and 8-bit rows at the start of x's rows), few rows and as many as the ring kernel takes: the
+    same bits as into memory of their own with the same strides (by which the order of a row's sum goes)."""
+    V, g = lib(), gen(53)
+    dt = DT[xt]
+    x = randn(g, rows, D, dtype=dt)
+    w = (1 + randn(g, D, scale=0.3)).to(dt)
+    want = V.rms_norm(x, w, 1e-6)[0]
+    apart = [torch.empty_like(x).view(torch.uint8)[:, :D].view(E4M3) for _ in range(2)]
+    want8, want_s, _ = V.rms_norm(x, w, 1e-6, out=apart[0])
+    wq, wqs = V.quant_rows(x, out=apart[1])
+    y = x.clone()
+    assert torch.equal(V.rms_norm(y, w, 1e-6, out=y)[0], want)
+    for call, a, s in ((lambda x, o: V.rms_norm(x, w, 1e-6, out=o)[:2], want8, want_s),
+                       (lambda x, o: V.quant_rows(x, out=o), wq, wqs)):
+        y = x.clone()
+        o = y.view(torch.uint8)[:, :D].view(E4M3)
+        got, gs = call(y, o)
+        assert got.data_ptr() == y.data_ptr() and torch.equal(got.float(), a.float()) and torch.equal(gs, s)

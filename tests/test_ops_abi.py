@@ -342,3 +342,21 @@ print("C ABI")
         res = _python(code, tmp_path, CXX=cxx)
         assert res.returncode != 0 and "RuntimeError" in res.stderr, res.stderr[-2000:]
         assert (pkg / V.ops._build.LIB_NAME).exists() and not (pkg / "_vit_ops.so").exists()
+
+
+@pytest.mark.parametrize("kw", [
+    dict(ot=E4M3, sc=A),                               # 8-bit rows packed at the start of x's memory
+    dict(ot=E4M3, sc=A, xt=F32, wt=F32, old=128),
+    dict(xld=128),                                     # rows brought together in place
+    dict(r=2 * A, h=2 * A, rt=F32, rld=64, hld=128),
+    dict(xld=0),                                       # a broadcast row
+])
+def test_rms_norm_refuses_an_output_on_other_rows(kw):
+    """out on x, or residual_out on residual, where row i is not on row i: what a block writes, others still read."""
+    assert _norm(**kw) == V.VIT_E_SHAPE
+
+
+def test_quant_rows_refuses_an_output_on_other_rows():
+    f = ops._fn("quant_rows")
+    assert f(A, BF16, 64, 4, 64, A, 64, 2 * A, None) == V.VIT_E_SHAPE
+    assert f(A, F32, 64, 4, 64, A, 128, 2 * A, None) == V.VIT_E_SHAPE

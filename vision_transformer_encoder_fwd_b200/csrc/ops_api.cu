@@ -138,6 +138,14 @@ vit_status run_rows(const RowsParams& p, int x_type, int r_type, int w_type, cud
   } else if (p.h != nullptr) {
     return fail(VIT_E_INVALID_ARG, "residual_out without residual");
   }
+  // An output on an input: row i on row i, which one block reads before it writes, or rows of other blocks would
+  // be overwritten before these have read them
+  auto other_rows = [&](const void* o, int64_t o_bytes, const void* in, int64_t in_bytes) {
+    return o == in && p.rows > 1 && o_bytes != in_bytes;
+  };
+  const int64_t out_bytes = p.out_ld * static_cast<int64_t>(os), x_bytes = p.x_ld * static_cast<int64_t>(xs);
+  if (other_rows(p.out, out_bytes, p.x, x_bytes) || (p.r != nullptr && other_rows(p.h, p.h_ld, p.r, p.r_ld)))
+    return fail(VIT_E_SHAPE, "an output on its input has to have the input's rows (the same bytes from row to row)");
   const int rmode = p.r == nullptr ? 0 : (r_type == x_type ? 1 : 2);
   const RowAccess access = vec ? ROWS_VEC : shift ? ROWS_SHIFT : ROWS_SINGLE;
   cudaError_t e;
