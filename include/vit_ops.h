@@ -83,10 +83,11 @@ enum { VIT_ROPE_PLAIN = 0, VIT_ROPE_LINEAR = 1, VIT_ROPE_BASE = 2, VIT_ROPE_PART
 vit_status vit_op_rope_freqs(double base, int32_t pairs, int32_t axes, int32_t scaling, double factor,
                              double original_len, double beta_fast, double beta_slow, double *freqs);
 
-/* One tensor of heads [T, heads, head_dim] in and out (strides in elements); in == NULL: none. */
+/* One tensor of heads [T, heads, head_dim] in and out (strides in elements; 0 to read the same head or token
+ * again, while the heads of an output do not overlap); in == NULL: none. */
 typedef struct vit_rope_tensor {
   const void *in;
-  void *out; /* may be `in` */
+  void *out; /* may be `in`, with its strides; otherwise overlaps nothing that the call reads or writes */
   int64_t in_token, in_head, out_token, out_head;
   int32_t heads;
 } vit_rope_tensor;
@@ -111,7 +112,8 @@ vit_status vit_op_rope(const vit_rope_tensor *q, const vit_rope_tensor *k, vit_d
  * Rows of `out` outside every sequence are left as they are; whatever the key rows of no sequence
  * or past len_k hold (NaN included) does not matter.  V must be finite in a sequence's own rows.
  *   q [Tq, heads_q, head_dim], k, v [Tk, heads_k, head_dim], out as q: `type` bf16 or fp16, head_dim
- *   64 or 128, strides multiples of 8, pointers 16-byte aligned.
+ *   64 or 128, strides multiples of 8 (0 to read the same head or token again), pointers 16-byte aligned.
+ *   The heads of `out` overlap neither one another nor what the call reads.
  *   cu_q, cu_k: device int32 [n + 1], not decreasing; len_k: device int32 [n].  Read on the device
  *   (a captured call takes new lengths on replay); values outside the buffers are clamped.
  *   max_q: the longest query length if the caller knows it, 0 if not.  Only the choice of kernels

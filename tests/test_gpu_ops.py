@@ -1018,3 +1018,49 @@ def test_rows_on_their_inputs(rows, D, xt):
         o = y.view(torch.uint8)[:, :D].view(E4M3)
         got, gs = call(y, o)
         assert got.data_ptr() == y.data_ptr() and torch.equal(got.float(), a.float()) and torch.equal(gs, s)
+
+
+@pytest.mark.parametrize("what", ["kv head", "kv token", "q head", "q token"])
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("d", [64, 128])
+def test_attention_reads_broadcast_heads_and_tokens(kernel, d, what):
+    """A stride of 0 in q, or in k and v, is right in every kernel."""
+    V, g = lib(), gen(54)
+    n, hkv = 70, 2
+    q = randn(g, n, 4, d, dtype=torch.bfloat16)
+    k, v = randn(g, n, hkv, d, dtype=torch.bfloat16), randn(g, n, hkv, d, dtype=torch.bfloat16)
+    if what == "q head":
+        q = q[:, :1].expand(-1, 4, -1)
+    if what == "q token":
+        q = q[:1].expand(n, -1, -1)
+    if what == "kv token":
+        k, v = k[:1].expand(n, -1, -1), v[:1].expand(n, -1, -1)
+    args = by_kernel(kernel, k, v, cum([30, 40]), cum([30, 40]))
+    if what == "kv head":
+        args["k"], args["v"] = (t[:, :1].expand(-1, hkv, -1) for t in (args["k"], args["v"]))
+        k, v = k[:, :1].expand(-1, hkv, -1), v[:, :1].expand(-1, hkv, -1)
+    if what == "kv token":
+        args["k"], args["v"] = (t[:1].expand(args["k"].shape[0], -1, -1) for t in (k, v))
+    out = V.attention_packed(q, **args, causal=True)
+    V.op_poll()
+    check_attn(out, q, k, v, [0, 30], [0, 30], [30, 40], [30, 40], True, d ** -0.5)
+
+
+def test_outputs_that_overlap_are_refused():
+    V, g = lib(), gen(55)
+    q = randn(g, 20, 4, 64, dtype=torch.bfloat16)
+    cu = cum([20])
+    pos = torch.arange(20, device="cuda")
+    f = V.rope_freqs(10000.0, 64)
+    for shared in (torch.zeros(20, 1, 64, device="cuda", dtype=q.dtype).expand(-1, 4, -1),
+                   torch.zeros(1, 4, 64, device="cuda", dtype=q.dtype).expand(20, -1, -1)):
+        for call in (lambda: V.attention_packed(q, q, q, cu, cu, out=shared), lambda: V.rope(q, None, pos, f, out=(shared, None)),
+                     lambda: V.rope(shared, None, pos, f, out=(shared, None))):
+            with pytest.raises(V.VitError) as e:
+                call()
+            assert e.value.status == V.VIT_E_SHAPE
+        assert (shared == 0).all()
+    # read, they are fine
+    x = q[:, :1].expand(-1, 4, -1)
+    y, _ = V.rope(x, None, pos, f)
+    check_rope(y, x, pos, f, "half")

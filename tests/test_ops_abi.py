@@ -360,3 +360,44 @@ def test_quant_rows_refuses_an_output_on_other_rows():
     f = ops._fn("quant_rows")
     assert f(A, BF16, 64, 4, 64, A, 64, 2 * A, None) == V.VIT_E_SHAPE
     assert f(A, F32, 64, 4, 64, A, 128, 2 * A, None) == V.VIT_E_SHAPE
+
+
+@pytest.mark.parametrize("kw", [
+    dict(out_token=0), dict(out_head=0), dict(out_token=64), dict(out_head=32), dict(out_head=128),
+    dict(out_head=8 * 64, out_token=56),
+    dict(heads_q=3, heads_k=1, Tq=3, out_head=192, out_token=192),  # interleaved, a token on a head
+    dict(heads_q=3, heads_k=1, Tq=4, out_head=192, out_token=136),  # 2 * 192 and 3 * 136 are 24 values apart
+])
+def test_attention_refuses_an_output_that_overlaps_itself(kw):
+    assert ops._fn("attention_packed")(ctypes.byref(attn_args(**{"heads_q": 2, "heads_k": 2, **kw})), None) == V.VIT_E_SHAPE
+
+
+def test_overlap_rule_against_all_pairs():
+    """What attention and rope refuse as an overlapping output, against every pair of heads, for layouts with heads in
+    tokens, tokens in heads and interleaved.  No call gets past its checks: the positions (or cu_q) are missing."""
+    f = (ctypes.c_double * 32)(*([0.5] * 32))
+    seen = set()
+    for T in (1, 2, 3, 5):
+        for H in (1, 2, 3, 4):
+            for st in (0, 1, 3, 4, 6, 8, 9, 12, 17, 20):
+                for sh in (0, 2, 4, 5, 8, 10, 12, 16, 23):
+                    at = [t * st + h * sh for t in range(T) for h in range(H)]
+                    over = any(abs(a - b) < 4 for i, a in enumerate(at) for b in at[:i])
+                    seen.add(over)
+                    x = V.VitRopeTensor(A, 2 * A, H * 4, 4, st, sh, H)
+                    got = ops._fn("rope")(ctypes.byref(x), None, BF16, T, 4, 4, None, 0, 1, f, 0, 1.0, 0, None)
+                    assert got == (V.VIT_E_SHAPE if over else V.VIT_E_INVALID_ARG), (T, H, st, sh)
+    assert seen == {True, False}
+
+
+def test_rope_refuses_an_output_on_other_heads():
+    f = (ctypes.c_double * 32)(*([0.5] * 32))
+
+    def call(T, heads, in_token, in_head, out_token, out_head):
+        x = V.VitRopeTensor(A, A, in_token, in_head, out_token, out_head, heads)
+        return ops._fn("rope")(ctypes.byref(x), None, BF16, T, 64, 64, None, 0, 1, f, 0, 1.0, 0, None)
+    assert call(4, 2, 256, 64, 128, 64) == V.VIT_E_SHAPE      # brought together in place
+    assert call(4, 2, 128, 64, 64, 256) == V.VIT_E_SHAPE      # transposed in place
+    assert call(4, 2, 0, 64, 128, 64) == V.VIT_E_SHAPE
+    assert call(4, 2, 256, 64, 256, 64) == V.VIT_E_INVALID_ARG  # positions missing: nothing else is wrong
+    assert call(1, 2, 7, 64, 9, 64) == V.VIT_E_INVALID_ARG

@@ -27,6 +27,26 @@ size_t type_size(int t) { return t == VIT_DT_F32 ? 4 : (t == VIT_DT_E4M3 ? 1 : 2
 
 bool real_type(int t) { return t == VIT_DT_BF16 || t == VIT_DT_F16 || t == VIT_DT_F32; }
 
+// Whether vectors of `width` values at i * si + j * sj, 0 <= i < ni, 0 <= j < nj, share a value.
+bool overlap_itself(int64_t ni, int64_t si, int64_t nj, int64_t sj, int64_t width) {
+  si = std::abs(si);
+  sj = std::abs(sj);
+  if ((ni > 1 && si < width) || (nj > 1 && sj < width)) return true;
+  if (ni <= 1 || nj <= 1) return false;
+  const __int128 wi = si, wj = sj;
+  if (wi >= (nj - 1) * wj + width || wj >= (ni - 1) * wi + width) return false;  // one inside the other
+  // interleaved: for each distance along the shorter axis the nearest ones along the other
+  if (ni > nj) {
+    std::swap(ni, nj);
+    std::swap(si, sj);
+  }
+  for (int64_t i = 1; i < ni; ++i) {
+    const int64_t j = i * si / sj;
+    if ((j < nj && i * si - j * sj < width) || (j + 1 < nj && (j + 1) * sj - i * si < width)) return true;
+  }
+  return false;
+}
+
 int current_sms() {
   int dev = 0;
   cudaGetDevice(&dev);
@@ -513,6 +533,9 @@ vit_status vit_op_rope(const vit_rope_tensor* q, const vit_rope_tensor* k, vit_d
     if (t.heads < 0) return fail(VIT_E_SHAPE, "negative number of heads");
     if (!t.out || !aligned_to(t.in, type_size(type)) || !aligned_to(t.out, type_size(type)))
       return fail(VIT_E_INVALID_ARG, "output NULL, or a pointer not aligned to its type");
+    if (T > 0 && overlap_itself(T, t.out_token, t.heads, t.out_head, head_dim)) return fail(VIT_E_SHAPE, "heads of an output overlap");
+    if (t.in == t.out && ((T > 1 && t.in_token != t.out_token) || (t.heads > 1 && t.in_head != t.out_head)))
+      return fail(VIT_E_SHAPE, "an output on its input has to have the input's strides");
     p.in[i] = t.in;
     p.out[i] = t.out;
     p.in_tok[i] = t.in_token;
@@ -592,6 +615,8 @@ vit_status vit_op_attention_packed(const vit_attn_packed* a, vit_stream_t stream
   const int64_t strides[8] = {a->q_token, a->q_head, a->k_token, a->k_head, a->v_token, a->v_head, a->out_token, a->out_head};
   for (int64_t s : strides)
     if (s % 8 || s < 0 || s >= (1LL << 38)) return fail(VIT_E_SHAPE, "strides must be multiples of 8, not negative");
+  if (overlap_itself(a->Tq, a->out_token, a->heads_q, a->out_head, a->head_dim))
+    return fail(VIT_E_SHAPE, "heads of out overlap");
   if (static_cast<int64_t>(a->n) + a->Tq > 0x7fffffffLL) return fail(VIT_E_SHAPE, "too many sequences");
   const AttnKernel which = attention_kernel(a);
   const bool rows = which == ATTN_SPLIT;
