@@ -1064,3 +1064,33 @@ def test_outputs_that_overlap_are_refused():
     x = q[:, :1].expand(-1, 4, -1)
     y, _ = V.rope(x, None, pos, f)
     check_rope(y, x, pos, f, "half")
+
+
+def test_written_tensors_show_in_autograd():
+    """What a call writes into counts as changed: a backward pass that saved it says so instead of using it."""
+    V, g = lib(), gen(56)
+    x, w = randn(g, 8, 64, dtype=torch.bfloat16), torch.ones(64, device="cuda")
+    q, cu = randn(g, 8, 2, 64, dtype=torch.bfloat16), cum([8])
+    pos, f = torch.arange(8, device="cuda"), V.rope_freqs(100.0, 64)
+    q8, s8 = V.quant_rows(randn(g, 8, 64))
+    res, out, o8, sc, k = randn(g, 8, 64), x.clone(), q8.clone(), s8.clone(), q.clone()
+    o2, s2, lin, att = q8.clone(), s8.clone(), torch.zeros(8, 8, device="cuda", dtype=torch.bfloat16), q.clone()
+    given = [res, out, o8, sc, q, k, o2, s2, lin, att]
+    before = [t._version for t in given]
+    V.rms_norm(x, w, residual=res, residual_out=res, out=out)
+    V.rms_norm(x, w, out=o8, scales=sc)
+    V.rope(q, k, pos, f, out=(q, k))
+    V.quant_rows(x, out=o2, scales=s2)
+    V.linear_fp8(q8, s8, q8, s8, out=lin)
+    V.attention_packed(q, q, q, cu, cu, out=att)
+    assert [t._version for t in given] == [v + 1 for v in before]
+    assert x._version == 0 and q8._version == 0
+    p = torch.ones(8, 64, device="cuda", requires_grad=True)
+    y = (p * res).sum()  # keeps res for p's gradient
+    V.rms_norm(x, w, residual=res, residual_out=res)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+    with torch.inference_mode():
+        frozen = torch.zeros(8, 64, device="cuda", dtype=torch.bfloat16)
+    V.rms_norm(x, w, out=frozen)  # has no version to count
+    assert torch.equal(frozen, V.rms_norm(x, w)[0])

@@ -401,3 +401,34 @@ def test_rope_refuses_an_output_on_other_heads():
     assert call(4, 2, 0, 64, 128, 64) == V.VIT_E_SHAPE
     assert call(4, 2, 256, 64, 256, 64) == V.VIT_E_INVALID_ARG  # positions missing: nothing else is wrong
     assert call(1, 2, 7, 64, 9, 64) == V.VIT_E_INVALID_ARG
+
+
+def test_binding_refuses_what_autograd_would_record():
+    """The operators are forward only: with grad mode on, a tensor that requires a gradient is refused, and without it
+    the call gets on (here to the check of the device)."""
+    bf = torch.bfloat16
+    x, w = torch.zeros(2, 16, dtype=bf), torch.ones(16)
+    heads, cu = torch.zeros(2, 1, 64, dtype=bf), torch.zeros(2, dtype=torch.int32)
+    q8, s8 = torch.zeros(8, 16).to(torch.float8_e4m3fn), torch.ones(8)
+    pos, f = torch.zeros(2, dtype=torch.int32), V.rope_freqs(100.0, 64)
+    calls = [
+        (lambda t: V.rms_norm(t, w), x), (lambda t: V.rms_norm(x, t), w), (lambda t: V.rms_norm(x, w, residual=t), x),
+        (lambda t: V.rms_norm(x, w, out=t), x), (lambda t: V.quant_rows(t), x),
+        (lambda t: V.linear_fp8(q8, t, q8, s8), s8), (lambda t: V.linear_fp8(q8, s8, q8, s8, bias=t), s8),
+        (lambda t: V.rope(t, None, pos, f), heads), (lambda t: V.rope(heads, t, pos, f), heads),
+        (lambda t: V.rope(heads, None, pos, t), f),
+        (lambda t: V.attention_packed(t, heads, heads, cu, cu), heads), (lambda t: V.attention_packed(heads, heads, t, cu, cu), heads),
+    ]
+    for call, t in calls:
+        leaf = t.clone().requires_grad_()
+        for needs in (leaf, leaf * 1):
+            with pytest.raises(V.VitError) as e:
+                call(needs)
+            assert e.value.status == V.VIT_E_UNSUPPORTED and "gradient" in str(e.value)
+        for context in (torch.no_grad(), torch.inference_mode()):
+            with context, pytest.raises(V.VitError) as e:
+                call(leaf)
+            assert e.value.status == V.VIT_E_INVALID_ARG
+        with pytest.raises(V.VitError) as e:
+            call(leaf.detach())
+        assert e.value.status == V.VIT_E_INVALID_ARG

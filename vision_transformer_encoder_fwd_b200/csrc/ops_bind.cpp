@@ -6,6 +6,7 @@
 #include <Python.h>
 
 #include <ATen/Functions.h>
+#include <ATen/core/grad_mode.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -74,12 +75,23 @@ PyObject* wrap_or_none(const std::optional<at::Tensor>& t) {
   Py_RETURN_NONE;
 }
 
+// The operators keep no history: a call that autograd would expect one of is refused.
+void need_no_history(const char* fn, Opt t) {
+  if (t != nullptr && t->requires_grad() && at::GradMode::is_enabled())
+    fail(fn, VIT_E_UNSUPPORTED, "forward only: a tensor requires a gradient (call under torch.no_grad(), or detach it)");
+}
+// A tensor of the caller's that was written: autograd sees that what it may have saved of it has changed.
+void written(Opt t) {
+  if (t != nullptr && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
+}
+
 // The tensors' device, which becomes the current one, and the stream (None: the device's current one),
 // which becomes the current one where it is given: allocations belong to it.
 class Place {
  public:
   Place(const char* fn, PyObject* stream, std::initializer_list<Opt> tensors) {
     c10::Device dev(c10::DeviceType::CPU);
+    for (Opt t : tensors) need_no_history(fn, t);
     for (Opt t : tensors) {
       if (t == nullptr) continue;
       if (!t->is_cuda()) fail(fn, VIT_E_INVALID_ARG, "tensors must be on a CUDA device");
@@ -192,6 +204,9 @@ PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
                             w.data_ptr(), type_of(fn, w), static_cast<float>(eps), rows, int32_of(fn, D), out.data_ptr(),
                             type_of(fn, out), leading(fn, out), sc ? static_cast<float*>(sc->data_ptr()) : nullptr,
                             at.handle()));
+  written(out_in);
+  written(sc_in);
+  written(h_in);
   return Py_BuildValue("(NNN)", out_in ? Py_NewRef(a[6]) : THPVariable_Wrap(out), sc_in ? Py_NewRef(a[7]) : wrap_or_none(sc),
                        r && h_in ? Py_NewRef(a[4]) : wrap_or_none(h));
   END_HANDLE_TH_ERRORS
@@ -214,6 +229,8 @@ PyObject* quant_rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
   need_type(fn, sc, at::kFloat, "scales must be fp32");
   check(fn, vit_op_quant_rows(x.data_ptr(), type_of(fn, x), x_ld, rows, int32_of(fn, D), out.data_ptr(), leading(fn, out),
                               static_cast<float*>(sc.data_ptr()), at.handle()));
+  written(out_in);
+  written(sc_in);
   return Py_BuildValue("(NN)", out_in ? Py_NewRef(a[1]) : THPVariable_Wrap(out),
                        sc_in ? Py_NewRef(a[2]) : THPVariable_Wrap(sc));
   END_HANDLE_TH_ERRORS
@@ -253,6 +270,7 @@ PyObject* linear_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
                               static_cast<const float*>(sw.data_ptr()), static_cast<const float*>(ptr(bias)),
                               int32_of(fn, M), int32_of(fn, N), int32_of(fn, K), out.data_ptr(), leading(fn, out),
                               status_word(fn, status), static_cast<uint64_t>(integer(a[8])), at.handle()));
+  written(out_in);
   return out_in ? Py_NewRef(a[5]) : THPVariable_Wrap(out);
   END_HANDLE_TH_ERRORS
 }
@@ -277,6 +295,7 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int32_t layout = int32_of(fn, integer(a[4]));
   const double gain = number(a[5]);
   const bool inverse = truth(a[6]);
+  need_no_history(fn, &f);
   Place at(fn, a[9], {&q, k, &pos, qo_in, ko_in});
   if (q.dim() != 3) fail(fn, VIT_E_SHAPE, "q must be [T, heads, head_dim]");
   const int64_t T = q.size(0), d = q.size(2);
@@ -303,6 +322,8 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
                         pos.data_ptr(), pos.scalar_type() == at::kLong ? 1 : 0, int32_of(fn, axes),
                         static_cast<const double*>(f.data_ptr()), layout, static_cast<float>(gain), inverse ? 1 : 0,
                         at.handle()));
+  written(qo_in);
+  written(ko_in);
   return Py_BuildValue("(NN)", qo_in ? Py_NewRef(a[7]) : THPVariable_Wrap(qo), k && ko_in ? Py_NewRef(a[8]) : wrap_or_none(ko));
   END_HANDLE_TH_ERRORS
 }
@@ -376,6 +397,7 @@ PyObject* attention_packed(PyObject*, PyObject* const* a, Py_ssize_t n) {
     p.workspace_bytes = need;
   }
   check(fn, vit_op_attention_packed(&p, at.handle()));
+  written(out_in);
   return out_in ? Py_NewRef(a[9]) : THPVariable_Wrap(out);
   END_HANDLE_TH_ERRORS
 }

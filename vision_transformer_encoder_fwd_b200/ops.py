@@ -5,7 +5,8 @@ Argument marshalling only, as in the rest of the binding, here by an extension m
 (csrc/ops_bind.cpp), since a single token's operators take a few microseconds: the work runs in the
 library's kernels on the tensors' device, on `stream` or on that device's current stream.  What a
 call refuses raises VitError with the library's status.  Outputs that are not given are allocated
-with torch, on the stream the call runs on.
+with torch, on the stream the call runs on.  Forward only: with grad mode on, a tensor that requires a gradient
+is refused.
 """
 from __future__ import annotations
 
