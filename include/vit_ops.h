@@ -96,7 +96,8 @@ typedef struct vit_rope_tensor {
  * axis a = i / (pairs / axes); the values past rotary_dim are copied.
  *   (x, y) -> gain * (x cos - y sin, x sin + y cos);  inverse != 0: by minus the angle (which is
  *   also the gradient's rotation).
- *   positions: device [axes, T], int32, or int64 if pos64 (any value; whole turns drop out exactly).
+ *   positions: device [axes, T], int32, or int64 if pos64.  Whole turns drop out exactly; for freqs up to 1 the
+ *   angle is off by at most 2^-33 + |position| 2^-64 turns (and the sine's fp32): 1.5e-9 rad up to 2^31.
  *   freqs: HOST array of rotary_dim / 2 doubles, radians per position, read during the call.
  *   rotary_dim: even, 2..256, <= head_dim, rotary_dim / 2 a multiple of axes; axes 1..4. */
 vit_status vit_op_rope(const vit_rope_tensor *q, const vit_rope_tensor *k, vit_dtype type, int64_t T, int32_t head_dim,

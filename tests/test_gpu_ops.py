@@ -1094,3 +1094,18 @@ def test_written_tensors_show_in_autograd():
         frozen = torch.zeros(8, 64, device="cuda", dtype=torch.bfloat16)
     V.rms_norm(x, w, out=frozen)  # has no version to count
     assert torch.equal(frozen, V.rms_norm(x, w)[0])
+
+
+def test_rope_rounds_the_angle():
+    """Angles of a few 2^-32 turns: the fraction of a turn is rounded to 2^-32, not cut, so that it is off by at most
+    2^-33 turns (and the sine by two units in its last place)."""
+    V = lib()
+    k = torch.arange(0, 64, dtype=torch.float64)
+    f = 2 * math.pi * (k + 0.75) * 2.0 ** -32
+    x = torch.zeros(2, 1, 128, device="cuda")
+    x[..., :64] = 1
+    pos = torch.tensor([1, -1], device="cuda")
+    out, _ = V.rope(x, None, pos, f)
+    t = torch.stack([f, -f]).cuda()
+    err = (out[:, 0, 64:].double() - torch.sin(t)).abs()
+    assert (err <= 2 * math.pi * 2.0 ** -33 * 1.01 + 4 * 2.0 ** -24 * t.abs()).all(), err.max().item()

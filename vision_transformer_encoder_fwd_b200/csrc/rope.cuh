@@ -2,10 +2,11 @@
 // t = position * frequency, (a cos t - b sin t, a sin t + b cos t); the rest of the head is copied.
 //
 // The angle never exists as a floating number.  The host turns a frequency f (radians per position)
-// into the 64-bit fixed-point fraction of a turn F = round(2^64 frac(f / 2 pi)); position * F
-// modulo 2^64 is then the exact fraction of a turn at any 64-bit position, with whole turns gone
-// by the wrap of unsigned multiplication, and only its top 32 bits go to sincospif (off by at most
-// 2^-33 turn, plus 2^-25 of the result by the conversion to fp32).
+// into the 64-bit fixed-point fraction of a turn F = 2^64 frac(f / 2 pi), off by at most 1 unit for frequencies up
+// to 1 and 3 up to 2 pi (f / 2 pi in the 64 bits of long double, then rounded).  position * F modulo 2^64 is the
+// fraction of a turn: whole turns are gone by the wrap of unsigned multiplication, and F's error counts
+// position times (|position| 2^-64 turns: 2^-33 at 2^31, 2^-24 at 2^40).  Rounded to 32 bits, off by at most
+// 2^-33 turn more, it goes to sincospif (by the conversion to fp32 2^-25 of it).
 //
 // Bound: bytes (q and k in and out).  A block takes a few tokens; its threads first compute the
 // tokens' cosines and sines once into shared memory, then each thread keeps those of its pairs
@@ -116,8 +117,8 @@ __global__ void __launch_bounds__(ROPE_THREADS, (HALF || E == 1) ? 4 : 5) rope_k
     const int64_t from = static_cast<int64_t>(j / per_axis) * p.T + tok0 + t;
     const long long pos = p.pos64 ? static_cast<const long long*>(p.pos)[from] : static_cast<const int*>(p.pos)[from];
     const unsigned long long ph = static_cast<unsigned long long>(pos) * p.turn[j];
-    // the top 32 bits as a signed fraction of a turn in [-1/2, 1/2), times 2 (sincospi's half turns)
-    const float half_turns = static_cast<float>(static_cast<int>(ph >> 32)) * 4.656612873077393e-10f;
+    // rounded to 32 bits, as a signed fraction of a turn in [-1/2, 1/2), times 2 (sincospi's half turns)
+    const float half_turns = static_cast<float>(static_cast<int>((ph + 0x80000000ull) >> 32)) * 4.656612873077393e-10f;
     float s, c;
     sincospif(half_turns, &s, &c);
     cs[i] = make_float2(c * p.gain, s * p.gain * p.sign);
