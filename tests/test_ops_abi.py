@@ -432,3 +432,14 @@ def test_binding_refuses_what_autograd_would_record():
         with pytest.raises(V.VitError) as e:
             call(leaf.detach())
         assert e.value.status == V.VIT_E_INVALID_ARG
+
+
+def test_binding_refuses_a_negative_wait():
+    """As an unsigned limit it would be centuries: no wait is without a bound."""
+    q8, s8 = torch.zeros(8, 16).to(torch.float8_e4m3fn), torch.ones(8)
+    heads, cu = torch.zeros(2, 1, 64, dtype=torch.bfloat16), torch.zeros(2, dtype=torch.int32)
+    for call in (lambda: V.linear_fp8(q8, s8, q8, s8, wait_ns=-1),
+                 lambda: V.attention_packed(heads, heads, heads, cu, cu, wait_ns=-1)):
+        with pytest.raises(V.VitError, match="wait_ns") as e:
+            call()
+        assert e.value.status == V.VIT_E_INVALID_ARG

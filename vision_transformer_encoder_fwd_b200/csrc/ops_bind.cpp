@@ -243,6 +243,12 @@ int32_t* status_word(const char* fn, Opt status) {
   return static_cast<int32_t*>(status->data_ptr());
 }
 
+uint64_t wait_limit(const char* fn, PyObject* o) {
+  const long long v = integer(o);
+  if (v < 0) fail(fn, VIT_E_INVALID_ARG, "wait_ns must not be negative (every wait is bounded; 0: the default)");
+  return static_cast<uint64_t>(v);
+}
+
 // (a, a_scales, w, w_scales, bias, out, status, stream, wait_ns) -> out
 PyObject* linear_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -250,6 +256,7 @@ PyObject* linear_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
   need_args(n, 9);
   const at::Tensor &x = tensor(fn, a[0]), &sx = tensor(fn, a[1]), &w = tensor(fn, a[2]), &sw = tensor(fn, a[3]);
   Opt bias = tensor_or_none(fn, a[4]), out_in = tensor_or_none(fn, a[5]), status = tensor_or_none(fn, a[6]);
+  const uint64_t wait_ns = wait_limit(fn, a[8]);
   Place at(fn, a[7], {&x, &sx, &w, &sw, bias, out_in, status});
   const int64_t lda = leading(fn, x), ldw = leading(fn, w), M = x.size(0), K = x.size(1), N = w.size(0);
   need_type(fn, x, at::kFloat8_e4m3fn, "a must be e4m3");
@@ -269,7 +276,7 @@ PyObject* linear_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
   check(fn, vit_op_linear_fp8(x.data_ptr(), lda, static_cast<const float*>(sx.data_ptr()), w.data_ptr(), ldw,
                               static_cast<const float*>(sw.data_ptr()), static_cast<const float*>(ptr(bias)),
                               int32_of(fn, M), int32_of(fn, N), int32_of(fn, K), out.data_ptr(), leading(fn, out),
-                              status_word(fn, status), static_cast<uint64_t>(integer(a[8])), at.handle()));
+                              status_word(fn, status), wait_ns, at.handle()));
   written(out_in);
   return out_in ? Py_NewRef(a[5]) : THPVariable_Wrap(out);
   END_HANDLE_TH_ERRORS
@@ -337,6 +344,7 @@ PyObject* attention_packed(PyObject*, PyObject* const* a, Py_ssize_t n) {
                    &cu_k = tensor(fn, a[4]);
   Opt len_k = tensor_or_none(fn, a[5]), out_in = tensor_or_none(fn, a[9]), status = tensor_or_none(fn, a[10]);
   const bool causal = truth(a[6]);
+  const uint64_t wait_ns = wait_limit(fn, a[12]);
   Place at(fn, a[11], {&q, &k, &v, &cu_q, &cu_k, len_k, out_in, status});
   if (q.dim() != 3 || k.dim() != 3 || v.sizes() != k.sizes() || q.size(2) != k.size(2))
     fail(fn, VIT_E_SHAPE, "q must be [Tq, heads_q, d], k and v [Tk, heads_k, d]");
@@ -387,7 +395,7 @@ PyObject* attention_packed(PyObject*, PyObject* const* a, Py_ssize_t n) {
   p.max_q = int32_of(fn, integer(a[8]));
   p.scale = a[7] == Py_None ? (d > 0 ? 1.0f / std::sqrt(static_cast<float>(d)) : 0.f) : static_cast<float>(number(a[7]));
   p.status = status_word(fn, status);
-  p.wait_ns = static_cast<uint64_t>(integer(a[12]));
+  p.wait_ns = wait_ns;
   size_t need = 0;
   check(fn, vit_op_attention_packed_workspace(&p, &need));
   at::Tensor ws;
