@@ -244,11 +244,13 @@ cudaError_t launch_lin8_tile(const CUtensorMap& a, const CUtensorMap& b, const C
 cudaError_t launch_lin8_pair(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o, const Lin8Params& p, int* st,
                              cudaStream_t s, int nsm) {
   static std::atomic<uint64_t> attr_done{0};
-  static std::atomic<int> max_clusters{0};
+  static std::atomic<int> max_clusters[64];  // by device
   constexpr int smem = Lin8PairCfg::SMEM_BYTES;
   cudaError_t e = set_smem_attr_once(lin8_pair_kernel, smem, attr_done);
   if (e != cudaSuccess) return e;
-  int mc = max_clusters.load();
+  int dev = 0;
+  cudaGetDevice(&dev);
+  int mc = max_clusters[dev & 63].load();
   if (mc == 0) {
     // how many 2-CTA clusters fit on the device at once (an SM can be left without a partner)
     cudaLaunchConfig_t cfg = {};
@@ -269,7 +271,7 @@ cudaError_t launch_lin8_pair(const CUtensorMap& a, const CUtensorMap& b, const C
       n = nsm / 2;
     }
     mc = std::max(1, std::min(n, nsm / 2));
-    max_clusters.store(mc);
+    max_clusters[dev & 63].store(mc);
   }
   const long long tiles = static_cast<long long>((p.M + 255) / 256) * ((p.N + 255) / 256);
   return launch_pdl(lin8_pair_kernel, dim3(static_cast<unsigned>(2 * std::min<long long>(tiles, mc))), dim3(LIN8_THREADS), smem,
