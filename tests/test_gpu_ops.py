@@ -1109,3 +1109,107 @@ def test_rope_rounds_the_angle():
     t = torch.stack([f, -f]).cuda()
     err = (out[:, 0, 64:].double() - torch.sin(t)).abs()
     assert (err <= 2 * math.pi * 2.0 ** -33 * 1.01 + 4 * 2.0 ** -24 * t.abs()).all(), err.max().item()
+
+
+def _fresh_process(code, **env):
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    return subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300,
+                          env={**os.environ, **env})
+
+
+EVERY_KERNEL = """
+import torch, vision_transformer_encoder_fwd_b200 as V
+torch.manual_seed(0)
+bf, dev = torch.bfloat16, "cuda"
+W = V.quant_rows(torch.randn(1024, 2048, device=dev))
+xs = {M: torch.randn(M, 2048, device=dev, dtype=bf) for M in (3, 40, 300, 9000)}
+res = {M: torch.randn(M, 2048, device=dev) for M in xs}
+wn = torch.rand(2048, device=dev) + 0.5
+k = torch.randn(5000, 2, 128, device=dev, dtype=bf)
+q = torch.randn(90, 4, 128, device=dev, dtype=bf)
+i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device=dev)
+f = V.rope_freqs(10000.0, 128)
+pos = torch.arange(90, device=dev)
+
+def every():
+    out = []
+    for M, x in xs.items():  # rows, K split, tile and pair kernels; rows in registers and through the ring
+        a, s, h = V.rms_norm(x, wn, 1e-6, residual=res[M], fp8=True)
+        out += [a.float(), s, h, V.linear_fp8(a, s, *W), V.linear_fp8(*V.quant_rows(x), *W)]
+    r, kr = V.rope(q, k[:90], pos, f)
+    out += [r, kr, V.attention_packed(r, kr, kr, i32(0, 50, 90), i32(0, 50, 90), causal=True, max_q=0)]
+    out.append(V.attention_packed(r[:2], k, k, i32(0, 1, 2), i32(0, 2500, 5000), max_q=1))
+    out.append(V.attention_packed(r[:40], k[:40], k[:40], i32(0, 20, 40), i32(0, 20, 40), causal=True, max_q=20))
+    return out
+"""
+
+
+def test_operators_without_early_starts(tmp_path):
+    """Launched in plain stream order (VIT_B200_PDL=0) the operators give the same bits."""
+    lib()
+    for pdl in ("0", "1"):
+        res = _fresh_process(EVERY_KERNEL + f"torch.save([t.cpu() for t in every()], {str(tmp_path / pdl)!r})\nV.op_poll()",
+                             VIT_B200_PDL=pdl)
+        assert res.returncode == 0, res.stderr[-2000:]
+    a, b = (torch.load(tmp_path / p) for p in "01")
+    assert len(a) == len(b) and all(torch.isfinite(x.float()).all() and torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_operators_from_several_threads():
+    """First calls and later ones from four threads at once, each on a stream of its own: the bits of calls one by one."""
+    lib()
+    res = _fresh_process(EVERY_KERNEL + """
+import threading
+start, bad, got = threading.Barrier(4), [], {}
+torch.cuda.synchronize()
+
+def work(me):
+    try:
+        with torch.cuda.stream(torch.cuda.Stream()):
+            start.wait()
+            got[me] = [every() for _ in range(8)]
+            torch.cuda.current_stream().synchronize()
+    except BaseException as e:
+        bad.append(e)
+
+threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+[t.start() for t in threads]
+[t.join() for t in threads]
+assert not bad, bad
+V.op_poll()
+want = every()
+for me, rounds in got.items():
+    for r in rounds:
+        assert all(torch.equal(x, y) for x, y in zip(r, want)), me
+print("fine")
+""")
+    assert res.returncode == 0 and "fine" in res.stdout, res.stderr[-2000:]
+
+
+def test_rows_and_layers_captured():
+    """The norm, 8-bit rows and 8-bit layers of every size captured into one graph and replayed on new values."""
+    V, g = lib(), gen(57)
+    w, sw = V.quant_rows(randn(g, 1024, 2048))
+    wn = 1 + randn(g, 2048, scale=0.2)
+    xs = [randn(g, M, 2048, dtype=torch.bfloat16) for M in (3, 40, 300, 9000)]
+
+    def run():
+        res = []
+        for x in xs:
+            a, s, _ = V.rms_norm(x, wn, 1e-6, fp8=True)
+            q, t = V.quant_rows(x)
+            res.append((a, s, V.linear_fp8(a, s, w, sw), q, t, V.linear_fp8(q, t, w, sw)))
+        return res
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run()
+    for _ in range(2):
+        for x in xs:
+            x.copy_(randn(g, *x.shape, dtype=torch.bfloat16, scale=3.0))
+        graph.replay()
+        for a, b in zip(got, run()):
+            assert all(torch.equal(x.float(), y.float()) for x, y in zip(a, b))
+    V.op_poll()
