@@ -96,8 +96,10 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // that rstd drops out and only the quotient is rounded.  `amax` is top rstd; below the smallest one the
 // scale is that one's.  There, and where 448 / top is past fp32's range, the factor itself need not have a
 // number in fp32 (rstd * 448 / 2^-100 from rstd = 6e5 on, which a row of zeros has for eps = 1e-12): v is brought
-// to y = v rstd first (`first`, 1 elsewhere), whose factor 448 / amax is at most 448 * 2^100.  A NaN as
-// amax, which is the scale's, is every value's.
+// to y = v rstd first (`first`, 1 elsewhere), whose factor 448 / amax is at most 448 * 2^100.  rows_kernel
+// multiplies by both everywhere (1 % of its time; a loop of its own for such rows spilled registers: 8191 rows of 4096,
+// bf16 residual, 53 us against 48), the ring kernel, which its instructions bound, only where it has to.  A NaN
+// as amax, which is the scale's, is every value's.
 __device__ __forceinline__ float row_factor(float top, float rstd, float amax, float& first) {
   float f = kE4m3Max / top;
   first = 1.0f;
@@ -228,23 +230,15 @@ __global__ void __launch_bounds__(rows_threads(E, NV, RMODE, SHIFT), rows_blocks
   }
   if (!live) return;
   const float rstd = norm ? rsqrtf(ss / static_cast<float>(p.D) + p.eps) : 1.0f;
-  float mul = rstd;
+  float mul = rstd, first = 1.0f;
   if (OUT8) {
     const float amax = top * rstd;
-    float first;
     mul = row_factor(top, rstd, amax, first);
-    if (first != 1.0f) {
-      he *= first;
-#pragma unroll
-      for (int v = 0; v < NV; ++v)
-#pragma unroll
-        for (int i = 0; i < E; ++i) h[v][i] *= first;
-    }
     if (t == 0) p.scales[row] = max_nan(amax, kRowAmaxMin) / kE4m3Max;
   }
   if (SHIFT && extra >= 0) {
     if (OUT8)
-      static_cast<uint8_t*>(p.out)[row * p.out_ld + extra] = static_cast<uint8_t>(e4m3x2(he * mul, 0.f));
+      static_cast<uint8_t*>(p.out)[row * p.out_ld + extra] = static_cast<uint8_t>(e4m3x2(he * first * mul, 0.f));
     else
       static_cast<TX*>(p.out)[row * p.out_ld + extra] = from_f32<TX>(he * mul);
   }
@@ -253,7 +247,7 @@ __global__ void __launch_bounds__(rows_threads(E, NV, RMODE, SHIFT), rows_blocks
     const int c = begin + (v * tpr + t) * E;
     if (c >= end) continue;
 #pragma unroll
-    for (int i = 0; i < E; ++i) h[v][i] *= mul;
+    for (int i = 0; i < E; ++i) h[v][i] = OUT8 ? h[v][i] * first * mul : h[v][i] * mul;
     if (OUT8) {
       uint8_t* o = static_cast<uint8_t*>(p.out) + row * p.out_ld + c;
       if constexpr (E == 8) {
