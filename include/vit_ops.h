@@ -3,7 +3,7 @@
  * tower, a decoder over patch tokens or a packed batch of images needs next to the encoder.
  * Attention over packed sequences (grouped heads, causal or full, whole prompts and single tokens
  * over a cache), rotary positions, the root-mean-square norm with the residual's addition, and
- * linear layers on 8-bit rows.
+ * linear layers on 8-bit rows.  Forward only: no operator has a backward pass (vit_op_rope's inverse is its own).
  *
  * Conventions as in vit.h: caller-owned device memory of the current device, work enqueued on
  * `stream` without synchronising, host validation before any launch.  Nothing is allocated and
@@ -117,14 +117,18 @@ vit_status vit_op_rope(const vit_rope_tensor *q, const vit_rope_tensor *k, vit_d
  *   The heads of `out` overlap neither one another nor what the call reads.
  *   cu_q, cu_k: device int32 [n + 1], not decreasing; len_k: device int32 [n].  Read on the device
  *   (a captured call takes new lengths on replay); values outside the buffers are clamped.
- *   max_q: the longest query length if the caller knows it, 0 if not.  Only the choice of kernels
- *   goes by it, with n, Tk and the heads (few query rows over long key rows, as single tokens over a
- *   cache, run on a kernel that splits the keys' axis over the GPU, short sequences on one without
- *   shared memory): a wrong value costs time, not results.
+ *   max_q: the longest query length if the caller knows it, 0 if not.  The choice between three kernels
+ *   goes by it, with n, Tk / n (the key rows a sequence has on average) and the heads: few query rows over long
+ *   key rows, as single tokens over a cache, run on one that splits the keys' axis over the GPU (one
+ *   token over 100003 keys, 32 heads on 8 of 128: 77 us; 1000 us with max_q = 0, since then tiles of 128 rows are
+ *   taken, each of which walks its keys alone), short sequences on one without shared memory.  Any value
+ *   is right; it decides the time, and within the precision below the last bits of the result.
  *   workspace: vit_op_attention_packed_workspace bytes of device memory, 16-byte aligned, that no
  *   other call uses before this one has run; needs no preparation.
- * Scores, softmax statistics and sums are fp32; the softmax weights are rounded to `type` for
- * the product with V (few query rows or short sequences: to twice its precision), the result once. */
+ * Scores, softmax statistics and sums are fp32.  The kernel of tiles rounds the softmax's weights to
+ * `type` for the product with V, the two others to twice its precision; the result is rounded once.  Bits are the
+ * same from call to call, but not between the kernels, so that a sequence's result can differ in its last bits
+ * with the batch it is in. */
 typedef struct vit_attn_packed {
   const void *q, *k, *v;
   void *out;

@@ -22,7 +22,7 @@
 // barriers) and K and V in hand before it waits for P.  The running maximum moves only when it grows by
 // more than 2^8.
 // Measured: 8 x 4101 tokens, 16 heads of 64, 734 us (751 TFLOP/s); 2 x 8192, 16 heads of 128, 875 us (1257
-// TFLOP/s); a causal prompt of 8191, 32 heads on 8 of 128, 538 us (1021 TFLOP/s).
+// TFLOP/s); a causal prompt of 8191, 32 heads on 8 of 128, 536-541 us (1020 TFLOP/s).
 // What a tile reads past its sequence's last key belongs to somebody else or to nobody and may be
 // NaN: scores there are replaced before use, and V's rows there are overwritten with zeros in
 // shared memory, since 0 * NaN would reach every row of O.
@@ -216,8 +216,9 @@ struct AttnPackedCfg {
   static_assert(8 * (UNITS + 2 * DONE + 4) + 8 + 8 * 4 <= 512, "barrier area");
 };
 
-// 2^x for a pair on the FMA pipe, as exp2_fma2, but with a NaN kept and exactly 0 from -126.5 down: the clamp
-// gives j = -127, whose power of two has no exponent bits.
+// 2^x for a pair on the FMA pipe, as exp2_fma2 (off by at most 7.5e-5 of the value, a sixth of what rounding P to
+// fp16 may take, less of bf16's), but with a NaN kept and exactly 0 from -126.5 down: the clamp gives j = -127,
+// whose power of two has no exponent bits.
 __device__ __forceinline__ float2 exp2_fma2_full(float2 x) {
   x.x = max_nan(x.x, -127.0f);
   x.y = max_nan(x.y, -127.0f);
@@ -233,7 +234,9 @@ __device__ __forceinline__ float2 exp2_fma2_full(float2 x) {
 }
 
 // P for 64 keys of one row: 2^(s c - mc), rounded, into 32 columns of tensor memory; with SUM returns the
-// sum of the unrounded values.  Masked scores are -infinity.  Every POLY-th pair of exponentials goes to the
+// sum of the unrounded values.  P has V's type because both operands of an MMA have one: half a step of it a
+// weight, which is the whole of the difference from 32-bit softmax (error against 64 bits, bf16: 2.3e-3 of the
+// result where rounding the result alone gives 1.7e-3).  A remainder as in attn_rows_kernel would double these MMAs.  Masked scores are -infinity.  Every POLY-th pair of exponentials goes to the
 // FMA pipe (4th at width 64, 8th at 128: 2nd to 16th were within 5 %, the 2nd slowest).
 template <typename T, bool SUM, int POLY>
 __device__ __forceinline__ float packed_p64(const float (&s)[64], float c, float mc, uint32_t t_p) {

@@ -17,7 +17,7 @@
 //     item, through the shared memory of its last stage.
 //   - P is kept as a pair of 16-bit numbers (value and remainder, two products with V): the matrix
 //     pipe has room to spare, and single tokens keep nearly fp32 accuracy.
-// Measured: 64 tokens over caches of 33 to 4096 keys, 32 heads on 8 of 128, 97 us (5.3 TB/s); one token over
+// Measured: 64 tokens over caches of 33 to 4096 keys, 32 heads on 8 of 128, 98-101 us (5.1-5.2 TB/s); one token over
 // 100003 keys 75 us (5.4 TB/s), over 400003 256 us (6.4 TB/s).
 // Scores past a row's last key are replaced before use; V's rows past the sequence's last key are
 // overwritten with zeros in shared memory (0 * NaN).

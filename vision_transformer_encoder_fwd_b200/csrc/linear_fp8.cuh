@@ -2,7 +2,7 @@
 // in e4m3, one fp32 scale per row of each, products accumulated in fp32.
 //
 // Four kernels:
-//   - lin8_rows_kernel for a few rows of A, bound by the weights' bytes (7 x 6144 x 4096: 6.3 us, 4.0 TB/s);
+//   - lin8_rows_kernel for a few rows of A, bound by the weights' bytes (7 x 6144 x 4096: 6.0 us, 4.2 TB/s);
 //   - lin8_tile_kernel, 128 x 128 tiles, one CTA per SM;
 //   - lin8_split_kernel, 128 x 128 tiles with K split over a cluster, where tiles are few (33 x 4096 x
 //     4096: 7.2 us, 12.9 unsplit);

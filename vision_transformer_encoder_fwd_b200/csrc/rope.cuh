@@ -12,8 +12,8 @@
 // tokens' cosines and sines once into shared memory, then each thread keeps those of its pairs
 // in registers and walks the heads with 16-byte accesses (8-byte ones or single values where
 // the layout asks for them), several heads' loads ahead of their use and the first of them ahead of the
-// sines.  16383 tokens of 40 heads of 128 in 16 bits, half of each head turned in interleaved pairs: 55 us
-// (6.1 TB/s), all of it in halves: 56 us; with one access in flight 86 and 96 us.
+// sines.  16383 tokens of 40 heads of 128 in 16 bits, half of each head turned in interleaved pairs: 57 us
+// call by call (5.8 TB/s), 55 replayed from a graph, all of it in halves 56; with one access in flight 86 and 96 us.
 #pragma once
 
 #include "rows.cuh"

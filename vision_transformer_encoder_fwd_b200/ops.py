@@ -159,9 +159,11 @@ def attention_packed(q, k, v, cu_q, cu_k, len_k=None, causal: bool = False, scal
     last that are multiples of 8.  Sequence i has query rows cu_q[i] .. cu_q[i+1] - 1 and key rows
     cu_k[i] .. cu_k[i+1] - 1 (int32 [n + 1] on the device), of which the first len_k[i] count if it
     is given (a cache: cu_k holds where each sequence's room begins).  causal: the last query
-    sees the last key.  scale: 1 / sqrt(d) by default.  max_q: the longest query length if known
-    (it picks kernels, not results).  Rows of out of no sequence are left as they are; an out
-    that is allocated here has arbitrary values there."""
+    sees the last key.  scale: 1 / sqrt(d) by default.  max_q: the longest query length if known; it
+    picks the kernel, and few queries over many keys (new tokens over a cache) are several times slower without
+    it.  Any value is right to the precision the header states; the last bits go by the kernel.
+    Rows of out of no sequence are left as they are; an out that is allocated here has arbitrary values
+    there."""
     return (_bind or _load()).attention_packed(q, k, v, cu_q, cu_k, len_k, causal, scale, max_q, out, status, stream,
                                                wait_ns)
 
