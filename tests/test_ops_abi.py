@@ -443,3 +443,14 @@ def test_binding_refuses_a_negative_wait():
         with pytest.raises(V.VitError, match="wait_ns") as e:
             call()
         assert e.value.status == V.VIT_E_INVALID_ARG
+
+
+def test_binding_that_does_not_name_its_torch_is_refused(monkeypatch):
+    """A module of an older checkout."""
+    if ops._bind is None:
+        ops._load()
+    with monkeypatch.context() as m:
+        m.delattr(ops._bind, "torch_version")
+        with pytest.raises(ImportError, match="built against torch an unknown version"):
+            ops._load()
+    ops._load()

@@ -88,9 +88,10 @@ def _load():
                               "start the process again")
     load_library()
     from . import _vit_ops
-    if _vit_ops.torch_version != torch.__version__:  # it reads tensors by the layout of the headers it was compiled with
-        raise ImportError(f"the operators' binding was built against torch {_vit_ops.torch_version}, this is "
-                          f"{torch.__version__}: run python {_build.__file__}")
+    built = getattr(_vit_ops, "torch_version", "an unknown version")
+    if built != torch.__version__:  # it reads tensors by the layout of the headers it was compiled with
+        raise ImportError(f"the operators' binding was built against torch {built}, this is {torch.__version__}: "
+                          f"run python {_build.__file__}")
     _vit_ops.set_error(VitError)
     _bind = _vit_ops
     return _bind
