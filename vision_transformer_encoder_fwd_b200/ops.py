@@ -164,7 +164,8 @@ def attention_packed(q, k, v, cu_q, cu_k, len_k=None, causal: bool = False, scal
     picks the kernel, and few queries over many keys (new tokens over a cache) are several times slower without
     it.  Any value is right to the precision the header states; the last bits go by the kernel.
     Rows of out of no sequence are left as they are; an out that is allocated here has arbitrary values
-    there."""
+    there.  k and v may hold anything outside the sequences' rows; v has to be finite in them, behind the
+    causal mask too."""
     return (_bind or _load()).attention_packed(q, k, v, cu_q, cu_k, len_k, causal, scale, max_q, out, status, stream,
                                                wait_ns)
 
